@@ -24,13 +24,17 @@ __all__ = [
     "rx_lp_reduce_scatter_chunk_bcast", "rx_lp_tree_chunk", "rx_allreduce_local",
     "rx_allreduce_local_workspace", "rx_allreduce_local_noalloc",
     "RX_NOALLOC_SCRATCH_BYTES", "RX_ALGO_AUTO", "RX_ALGO_FLAT", "RX_ALGO_TREE",
-    "RX_ALGO_LOWPREC", "EXPORTED_SYMBOLS",
+    "RX_ALGO_LOWPREC", "EXPORTED_SYMBOLS", "RX_INT8", "RX_MAX_TOPK", "RX_MAX_EXPERTS",
+    "rx_moe_dispatch", "rx_moe_dispatch_workspace", "rx_moe_combine", "rx_moe_combine_backward",
+    "rx_residual_norm", "rx_residual_norm_backward", "rx_residual_norm_backward_workspace",
+    "rx_quant_i8", "rx_gemm_i8",
 ]
 
-RX_FP32, RX_BF16, RX_FP8_E4M3, RX_FP8_E5M2 = 0, 1, 2, 3
+RX_FP32, RX_BF16, RX_FP8_E4M3, RX_FP8_E5M2, RX_INT8 = 0, 1, 2, 3, 4
 RX_DRR_SUM, RX_DRR_REQUANT = 0, 1
 RX_ALGO_AUTO, RX_ALGO_FLAT, RX_ALGO_TREE, RX_ALGO_LOWPREC = 0, 1, 2, 3
 RX_MAX_SRC = 16
+RX_MAX_TOPK, RX_MAX_EXPERTS = 64, 1024
 RX_NOALLOC_SCRATCH_BYTES = 64 << 20
 RX_ERR_SCRATCH = 6
 
@@ -40,7 +44,9 @@ EXPORTED_SYMBOLS = (
     "rx_lp_reduce_scatter_chunk_bcast", "rx_lp_tree_chunk", "rx_allreduce_local",
     "rx_allreduce_local_workspace", "rx_allreduce_local_noalloc", "rxtest_block_scale_bits", "rxtest_fp8_encode_bits", "rxtest_fp8_decode", "rxtest_bf16_round_bits",
     "rxtest_group_max", "rxtest_stream", "rxtest_stream_sink_bytes", "rxtest_stream_mixed",
-    "rxtest_copy_streams",
+    "rxtest_copy_streams", "rx_moe_dispatch", "rx_moe_dispatch_workspace", "rx_moe_combine",
+    "rx_moe_combine_backward", "rx_residual_norm", "rx_residual_norm_backward",
+    "rx_residual_norm_backward_workspace", "rx_quant_i8", "rx_gemm_i8",
 )
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -61,6 +67,7 @@ _P = ctypes.c_void_p
 _PP = ctypes.POINTER(ctypes.c_void_p)
 _SZ = ctypes.c_size_t
 _I = ctypes.c_int
+_F = ctypes.c_float
 
 
 def lib() -> ctypes.CDLL:
@@ -90,6 +97,18 @@ def lib() -> ctypes.CDLL:
             "rx_lp_tree_chunk": [_SZ, _I, _I, _I, ctypes.POINTER(_SZ), ctypes.POINTER(_SZ)],
             "rx_allreduce_local": [_PP, _I, _SZ, _I, _I, _I, _I, _P, _SZ, _P],
             "rx_allreduce_local_noalloc": [_PP, _I, _SZ, _I, _I, _I, _I, _P],
+            "rx_moe_dispatch": [_P, _SZ, _I, _I, _I, _P, _SZ, _SZ, _I, _P, _P, _P, _P, _SZ, _I, _P,
+                                _P, _SZ, _P],
+            "rx_moe_combine": [_P, _SZ, _SZ, _P, _P, _SZ, _I, _SZ, _I, _P, _SZ, _P],
+            "rx_moe_combine_backward": [_P, _SZ, _P, _SZ, _SZ, _P, _P, _P, _SZ, _I, _SZ, _I, _P,
+                                        _SZ, _P, _P],
+            "rx_residual_norm": [_PP, _I, _SZ, _P, _SZ, _P, _SZ, _P, _P, _F, _F, _SZ, _SZ, _I, _P,
+                                 _SZ, _P, _SZ, _P, _P, _P],
+            "rx_residual_norm_backward": [_PP, _I, _SZ, _P, _SZ, _P, _SZ, _P, _P, _P, _P, _F, _SZ,
+                                          _SZ, _I, _P, _SZ, _P, _SZ, _P, _SZ, _P, _SZ, _P, _P, _P,
+                                          _P, _SZ, _P],
+            "rx_quant_i8": [_P, _SZ, _SZ, _SZ, _I, _P, _SZ, _P, _P],
+            "rx_gemm_i8": [_P, _SZ, _P, _P, _SZ, _SZ, _P, _P, _I, _SZ, _SZ, _SZ, _P, _SZ, _I, _P],
             "rxtest_fp8_encode_bits": [ctypes.c_uint32, _SZ, _I, _P, _P],
             "rxtest_block_scale_bits": [ctypes.c_uint32, _SZ, _I, _P, _P, _P],
             "rxtest_fp8_decode": [_P, _SZ, _I, _P, _P],
@@ -107,6 +126,10 @@ def lib() -> ctypes.CDLL:
         L.rxtest_stream_sink_bytes.restype = ctypes.c_size_t
         L.rx_allreduce_local_workspace.argtypes = [_I, _SZ, _I]
         L.rx_allreduce_local_workspace.restype = ctypes.c_size_t
+        L.rx_moe_dispatch_workspace.argtypes = [_SZ, _I, _I]
+        L.rx_moe_dispatch_workspace.restype = ctypes.c_size_t
+        L.rx_residual_norm_backward_workspace.argtypes = [_SZ, _SZ, _SZ]
+        L.rx_residual_norm_backward_workspace.restype = ctypes.c_size_t
         L.rx_status_string.argtypes = [_I]
         L.rx_status_string.restype = ctypes.c_char_p
         _lib = L
@@ -352,6 +375,277 @@ def rx_allreduce_local_noalloc(bufs: Sequence, algo: int = RX_ALGO_AUTO, fmt="e4
     _check(lib().rx_allreduce_local_noalloc(_ptr_array([t.data_ptr() for t in bufs]), len(bufs),
                                             count, dt, int(algo), _fp8_code(fmt), block,
                                             _stream(stream)), "rx_allreduce_local_noalloc")
+
+
+# ---- the operators around a block's allreduce ---------------------------------
+
+def _check_block(index: int, dtype, shape, name: str, t) -> int:
+    """A GPU tensor of the given shape whose rows are packed (any row stride);
+    returns its row stride in elements."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a GPU tensor")
+    if t.get_device() != index:
+        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{index}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
+    if len(shape) < 2:
+        if shape and shape[0] > 1 and t.stride(0) != 1:
+            raise ValueError(f"{name} must be contiguous")
+        return 0
+    rows, width = shape[-2], shape[-1]
+    stride = t.stride()
+    if width > 1 and stride[-1] != 1:
+        raise ValueError(f"{name}'s rows must be contiguous")
+    ld = stride[-2]
+    if rows > 1 and ld < width:
+        raise ValueError(f"{name}'s rows overlap")
+    return ld if rows > 1 else max(ld, width)
+
+
+def _check_packed(index: int, dtype, shape, name: str, t) -> None:
+    _check_block(index, dtype, shape, name, t)
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+
+
+def _opt(t):
+    return None if t is None else t.data_ptr()
+
+
+def _workspace(workspace, index: int):
+    import torch
+    if workspace is None:
+        return None, 0
+    _check_packed(index, torch.uint8, workspace.shape, "workspace", workspace)
+    return workspace.data_ptr(), workspace.numel()
+
+
+def rx_moe_dispatch_workspace(tokens: int, topk: int, experts: int) -> int:
+    """Workspace bytes of rx_moe_dispatch (0: none is needed)."""
+    return int(lib().rx_moe_dispatch_workspace(tokens, topk, experts))
+
+
+def rx_moe_dispatch(expert_ids, experts: int, offsets, order, slots, x=None, rows=None,
+                    scales=None, first_expert: int = 0, workspace=None, stream=None) -> None:
+    """Tokens sorted by expert: expert_ids (int32, tokens x topk) gives offsets
+    (int32, experts + 1), order (int32, tokens topk) and slots (int32, tokens x
+    topk); with x (tokens x hidden), rows (tokens topk x hidden, x's dtype, or
+    int8 with scales, float32) receives the tokens in that order."""
+    import torch
+    dev, i32 = torch.cuda.current_device(), torch.int32
+    tokens, topk = expert_ids.shape
+    pairs = tokens * topk
+    _check_packed(dev, i32, (tokens, topk), "expert_ids", expert_ids)
+    _check_packed(dev, i32, (experts + 1,), "offsets", offsets)
+    _check_packed(dev, i32, (pairs,), "order", order)
+    _check_packed(dev, i32, (tokens, topk), "slots", slots)
+    hidden = ld_x = ld_rows = 0
+    xdt = rdt = RX_FP32
+    if x is not None or rows is not None or scales is not None:
+        if x is None or rows is None:
+            raise ValueError("x and rows come together")
+        hidden, xdt = x.shape[-1], _rx_dtype(x)
+        ld_x = _check_block(dev, x.dtype, (tokens, hidden), "x", x)
+        quant = rows.dtype == torch.int8
+        if quant != (scales is not None):
+            raise ValueError("scales come with int8 rows")
+        rdt = RX_INT8 if quant else xdt
+        ld_rows = _check_block(dev, torch.int8 if quant else x.dtype, (pairs, hidden), "rows", rows)
+        if quant:
+            _check_packed(dev, torch.float32, (pairs,), "scales", scales)
+    ws, nbytes = _workspace(workspace, dev)
+    _check(lib().rx_moe_dispatch(expert_ids.data_ptr(), tokens, topk, first_expert, experts, _opt(x),
+                                 ld_x, hidden, xdt, offsets.data_ptr(), order.data_ptr(),
+                                 slots.data_ptr(), _opt(rows), ld_rows, rdt, _opt(scales), ws, nbytes,
+                                 _stream(stream)), "rx_moe_dispatch")
+
+
+def rx_moe_combine(rows, slots, weights, out, stream=None) -> None:
+    """out[t] = sum over j of weights[t, j] rows[slots[t, j]] (dropped pairs left
+    out); weights float32, or None for ones: the gradient of rx_moe_dispatch's
+    gather."""
+    import torch
+    dev = torch.cuda.current_device()
+    tokens, topk = slots.shape
+    nrows, hidden = rows.shape
+    dt = _rx_dtype(rows)
+    ld_rows = _check_block(dev, rows.dtype, (nrows, hidden), "rows", rows)
+    ld_out = _check_block(dev, rows.dtype, (tokens, hidden), "out", out)
+    _check_packed(dev, torch.int32, (tokens, topk), "slots", slots)
+    if weights is not None:
+        _check_packed(dev, torch.float32, (tokens, topk), "weights", weights)
+    _check(lib().rx_moe_combine(rows.data_ptr(), ld_rows, nrows, slots.data_ptr(), _opt(weights),
+                                tokens, topk, hidden, dt, out.data_ptr(), ld_out, _stream(stream)),
+           "rx_moe_combine")
+
+
+def rx_moe_combine_backward(d_out, rows, slots, weights, offsets, d_rows, d_weights=None,
+                            stream=None) -> None:
+    """Gradient of rx_moe_combine for a plan of rx_moe_dispatch: d_rows (rows that
+    no pair owns are 0) and, when given, d_weights (then rows are needed)."""
+    import torch
+    dev = torch.cuda.current_device()
+    tokens, topk = slots.shape
+    nrows, hidden = d_rows.shape
+    dt = _rx_dtype(d_out)
+    ld_g = _check_block(dev, d_out.dtype, (tokens, hidden), "d_out", d_out)
+    ld_dr = _check_block(dev, d_out.dtype, (nrows, hidden), "d_rows", d_rows)
+    ld_r = 0
+    if rows is not None:
+        ld_r = _check_block(dev, d_out.dtype, (nrows, hidden), "rows", rows)
+    elif d_weights is not None:
+        raise ValueError("d_weights needs rows")
+    _check_packed(dev, torch.int32, (tokens, topk), "slots", slots)
+    _check_packed(dev, torch.int32, offsets.shape, "offsets", offsets)
+    if offsets.numel() < 1:
+        raise ValueError("offsets must hold experts + 1 values")
+    for name, t in (("weights", weights), ("d_weights", d_weights)):
+        if t is not None:
+            _check_packed(dev, torch.float32, (tokens, topk), name, t)
+    _check(lib().rx_moe_combine_backward(
+        d_out.data_ptr(), ld_g, _opt(rows), ld_r, nrows, slots.data_ptr(), _opt(weights),
+        offsets.data_ptr() + 4 * (offsets.numel() - 1), tokens, topk, hidden, dt, d_rows.data_ptr(),
+        ld_dr, _opt(d_weights), _stream(stream)), "rx_moe_combine_backward")
+
+
+def _norm_inputs(srcs, residual, gate, gate_rows, w_post, w_pre):
+    """Checks what both directions of rx_residual_norm read; returns (device,
+    rows, hidden, dtype, gate_rows, source stride, residual stride)."""
+    import torch
+    dev = torch.cuda.current_device()
+    rows, hidden = srcs[0].shape
+    dtype = srcs[0].dtype
+    _rx_dtype(srcs[0])
+    ld_src = _check_block(dev, dtype, (rows, hidden), "srcs[0]", srcs[0])
+    for k in range(1, len(srcs)):
+        if _check_block(dev, dtype, (rows, hidden), "a source", srcs[k]) != ld_src:
+            raise ValueError(f"srcs[{k}] has another row stride than srcs[0]")
+    ld_res = 0
+    if residual is not None:
+        ld_res = _check_block(dev, dtype, (rows, hidden), "residual", residual)
+    if gate_rows is None:
+        gate_rows = max(1, rows)
+    if gate is not None:
+        if gate_rows < 1:
+            raise ValueError("gate_rows must be positive")
+        _check_packed(dev, dtype, (-(-rows // gate_rows), hidden), "gate", gate)
+    if w_post is not None:
+        _check_packed(dev, dtype, (hidden,), "w_post", w_post)
+    if w_pre is not None:
+        _check_packed(dev, dtype, (hidden,), "w_pre", w_pre)
+    return dev, rows, hidden, dtype, gate_rows, ld_src, ld_res
+
+
+def rx_residual_norm(srcs: Sequence, residual, gate, w_post, w_pre, out_h, out_z, rstd_post=None,
+                     rstd_pre=None, gate_rows: Optional[int] = None, residual_scale: float = 1.0,
+                     eps: float = 1e-6, stream=None) -> None:
+    """h = residual_scale residual + gate norm(sum of srcs) w_post, z = norm(h)
+    w_pre, RMS norms in FP32. residual, gate, w_post and one of out_h, out_z
+    may be None. gate has a row for every gate_rows rows (None: one row)."""
+    import torch
+    dev, rows, hidden, dtype, gate_rows, ld_src, ld_res = _norm_inputs(srcs, residual, gate,
+                                                                       gate_rows, w_post, w_pre)
+    ld_h = _check_block(dev, dtype, (rows, hidden), "out_h", out_h) if out_h is not None else 0
+    ld_z = _check_block(dev, dtype, (rows, hidden), "out_z", out_z) if out_z is not None else 0
+    if rstd_post is not None:
+        _check_packed(dev, torch.float32, (rows,), "rstd_post", rstd_post)
+    if rstd_pre is not None:
+        _check_packed(dev, torch.float32, (rows,), "rstd_pre", rstd_pre)
+    _check(lib().rx_residual_norm(
+        _ptr_array([s.data_ptr() for s in srcs]), len(srcs), ld_src, _opt(residual), ld_res,
+        _opt(gate), gate_rows, _opt(w_post), _opt(w_pre), residual_scale, eps, rows, hidden,
+        RX_BF16 if dtype == torch.bfloat16 else RX_FP32, _opt(out_h), ld_h, _opt(out_z), ld_z,
+        _opt(rstd_post), _opt(rstd_pre), _stream(stream)), "rx_residual_norm")
+
+
+def rx_residual_norm_backward_workspace(rows: int, hidden: int, gate_rows: Optional[int] = None) -> int:
+    """Workspace bytes of rx_residual_norm_backward."""
+    return int(lib().rx_residual_norm_backward_workspace(
+        rows, hidden, max(1, rows) if gate_rows is None else gate_rows))
+
+
+def rx_residual_norm_backward(srcs: Sequence, residual, gate, w_post, w_pre, rstd_post, rstd_pre,
+                              d_h, d_z, d_src, d_residual=None, d_gate=None, d_w_post=None,
+                              d_w_pre=None, gate_rows: Optional[int] = None,
+                              residual_scale: float = 1.0, workspace=None, stream=None) -> None:
+    """Gradient of rx_residual_norm from d_h and d_z (either may be None) and the
+    forward call's inputs and rstd_post, rstd_pre: d_src (every source's),
+    d_residual, and in float32 d_gate, d_w_post, d_w_pre; each of the last four
+    may be None."""
+    import torch
+    dev, rows, hidden, dtype, gate_rows, ld_src, ld_res = _norm_inputs(srcs, residual, gate,
+                                                                       gate_rows, w_post, w_pre)
+    f32 = torch.float32
+    lds = []
+    for name, t in (("d_h", d_h), ("d_z", d_z), ("d_src", d_src), ("d_residual", d_residual)):
+        lds.append(0 if t is None else _check_block(dev, dtype, (rows, hidden), name, t))
+    for name, t in (("rstd_post", rstd_post), ("rstd_pre", rstd_pre)):
+        if t is not None:
+            _check_packed(dev, f32, (rows,), name, t)
+    for name, t in (("d_w_post", d_w_post), ("d_w_pre", d_w_pre)):
+        if t is not None:
+            _check_packed(dev, f32, (hidden,), name, t)
+    if d_gate is not None:
+        _check_packed(dev, f32, (-(-rows // gate_rows), hidden), "d_gate", d_gate)
+    ws, nbytes = _workspace(workspace, dev)
+    _check(lib().rx_residual_norm_backward(
+        _ptr_array([s.data_ptr() for s in srcs]), len(srcs), ld_src, _opt(residual), ld_res,
+        _opt(gate), gate_rows, _opt(w_post), _opt(w_pre), _opt(rstd_post), _opt(rstd_pre),
+        residual_scale, rows, hidden, RX_BF16 if dtype == torch.bfloat16 else RX_FP32, _opt(d_h),
+        lds[0], _opt(d_z), lds[1], _opt(d_src), lds[2], _opt(d_residual), lds[3], _opt(d_gate),
+        _opt(d_w_post), _opt(d_w_pre), ws, nbytes, _stream(stream)), "rx_residual_norm_backward")
+
+
+def rx_quant_i8(x, codes, scales, stream=None) -> None:
+    """Rows of x (float32 or bfloat16) to int8 codes and a float32 scale a row."""
+    import torch
+    dev = torch.cuda.current_device()
+    rows, k = x.shape
+    dt = _rx_dtype(x)
+    ld_x = _check_block(dev, x.dtype, (rows, k), "x", x)
+    ld_c = _check_block(dev, torch.int8, (rows, k), "codes", codes)
+    _check_packed(dev, torch.float32, (rows,), "scales", scales)
+    _check(lib().rx_quant_i8(x.data_ptr(), ld_x, rows, k, dt, codes.data_ptr(), ld_c,
+                             scales.data_ptr(), _stream(stream)), "rx_quant_i8")
+
+
+def _check_padded(t, k: int, ld: int, name: str) -> None:
+    """The product reads whole 16-byte chunks: the last row's must lie in the
+    tensor's storage too."""
+    if k % 16 and t.numel():
+        last = t.storage_offset() + sum((n - 1) * s for n, s in zip(t.shape[:-1], t.stride()[:-1]))
+        if last + -(-k // 16) * 16 > t.untyped_storage().nbytes():
+            raise ValueError(f"{name}'s last row must be padded to a multiple of 16 bytes")
+
+
+def rx_gemm_i8(a, a_scales, b, b_scales, out, offsets=None, stream=None) -> None:
+    """out[m, j] = (sum over i of a[m, i] b[j, i]) a_scales[m] b_scales[j] for int8
+    a (rows x k) and b (n x k), or with offsets (int32, experts + 1, of
+    rx_moe_dispatch) b (experts x n x k), rows offsets[e] .. offsets[e + 1] - 1
+    times b[e]. Row strides are multiples of 16 (pad the rows)."""
+    import torch
+    dev, i8, f32 = torch.cuda.current_device(), torch.int8, torch.float32
+    rows, k = a.shape
+    n = b.shape[-2]
+    experts = b.shape[0] if offsets is not None else 1
+    shape = (n, k) if offsets is None else (experts, n, k)
+    ld_a = _check_block(dev, i8, (rows, k), "a", a)
+    ld_b = _check_block(dev, i8, shape, "b", b)
+    stride_b = 0
+    if offsets is not None:
+        _check_packed(dev, torch.int32, (experts + 1,), "offsets", offsets)
+        stride_b = b.stride(0)
+    _check_packed(dev, f32, (rows,), "a_scales", a_scales)
+    _check_packed(dev, f32, shape[:-1], "b_scales", b_scales)
+    dt = _rx_dtype(out)
+    ld_o = _check_block(dev, out.dtype, (rows, n), "out", out)
+    _check_padded(a, k, ld_a, "a")
+    _check_padded(b, k, ld_b, "b")
+    _check(lib().rx_gemm_i8(a.data_ptr(), ld_a, a_scales.data_ptr(), b.data_ptr(), ld_b, stride_b,
+                            b_scales.data_ptr(), _opt(offsets), experts, rows, n, k, out.data_ptr(),
+                            ld_o, dt, _stream(stream)), "rx_gemm_i8")
 
 
 # ---- test hooks (rx_testhooks.h) -------------------------------------------

@@ -7,8 +7,7 @@
 #include <stdio.h>
 #include <stdlib.h>
 
-#include "rx.h"
-#include "rx_internal.hpp"
+#include "api_checks.hpp"
 
 namespace rx {
 
@@ -75,36 +74,7 @@ static __device__ __align__(256) uint8_t scratch[RX_NOALLOC_SCRATCH_BYTES];
 
 namespace {
 
-constexpr size_t kMaxCount = (size_t)1 << 38;  // elements per buffer
-
-bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
-bool aligned4(const void* p) { return ((uintptr_t)p & 3u) == 0; }
-bool hp_type(rx_dtype_t t) { return t == RX_FP32 || t == RX_BF16; }
-bool fp8_type(rx_dtype_t t) { return t == RX_FP8_E4M3 || t == RX_FP8_E5M2; }
-bool valid_block(int b) { return b >= 32 && b <= 1024 && (b & (b - 1)) == 0; }
-
-// A failed launch is always reported on stderr with the HIP error's name.
-rx_status_t launched(hipError_t e)
-{
-    if (e == hipSuccess)
-        return RX_OK;
-    fprintf(stderr, "librx: launch failed: %s (%s)\n", hipGetErrorName(e), hipGetErrorString(e));
-    return RX_ERR_HIP;
-}
-
-// Shared checks of a source-pointer array: NULL array / entries, alignment.
-rx_status_t check_ptrs(const void* const* p, int n, bool align16)
-{
-    if (!p)
-        return RX_ERR_NULL;
-    for (int j = 0; j < n; ++j)
-        if (!p[j])
-            return RX_ERR_NULL;
-    for (int j = 0; j < n; ++j)
-        if (align16 ? !aligned16(p[j]) : !aligned4(p[j]))
-            return RX_ERR_ALIGN;
-    return RX_OK;
-}
+using namespace rx;
 
 size_t round256(size_t n) { return (n + 255u) / 256u * 256u; }
 
@@ -301,9 +271,9 @@ const char* rx_status_string(rx_status_t s)
     switch (s) {
     case RX_OK: return "RX_OK";
     case RX_ERR_NULL: return "RX_ERR_NULL: a required pointer is NULL";
-    case RX_ERR_ARG: return "RX_ERR_ARG: invalid nsrc, rank, block, mode or count";
+    case RX_ERR_ARG: return "RX_ERR_ARG: invalid nsrc, rank, block, mode, count, size or stride";
     case RX_ERR_DTYPE: return "RX_ERR_DTYPE: dtype not supported by this operation";
-    case RX_ERR_ALIGN: return "RX_ERR_ALIGN: buffer misaligned (16 B data, 4 B scales)";
+    case RX_ERR_ALIGN: return "RX_ERR_ALIGN: buffer misaligned (16 B data, 4 B scales, its element in strided rows)";
     case RX_ERR_HIP: return "RX_ERR_HIP: the HIP runtime rejected the launch";
     case RX_ERR_SCRATCH: return "RX_ERR_SCRATCH: the call needs more than the library's scratch";
     }

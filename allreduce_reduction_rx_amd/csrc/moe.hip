@@ -1,0 +1,518 @@
+// moe.hip -- tokens to the experts' rows and back (gfx950): the sort by
+// expert with its gather, the weighted combination, and its gradient. The
+// operations are defined in rx.h.
+//
+// All three move rows: their time is the rows' bytes over the memory rate at
+// prefill sizes and the latency of one dependent chain of loads at decode
+// sizes.
+//
+// The sort. The sorted place of pair i is a count: the pairs with a smaller
+// expert, and the pairs before i with the same one. Each token's workgroup
+// counts for its own topk pairs (compares and adds over ids that sit in L2),
+// so no ordering pass writes the order before the gather reads it, the
+// places come out stable, and they do not depend on timing. Up to kCountAll
+// pairs the count runs over all ids in the one launch that gathers. Above,
+// two small launches count experts per segment of kSegment pairs and sum
+// over segments, and a token counts in its own segment only.
+#include "block_common.hpp"
+
+namespace rx {
+namespace {
+
+constexpr int kGroup = 8;          // a token's pairs handled together
+constexpr int kSegment = 1024;     // pairs of a counting segment (rounded down to whole tokens)
+
+__device__ __forceinline__ int local_expert(int id, int first, int experts)
+{
+    const uint32_t e = (uint32_t)id - (uint32_t)first;   // ids below `first` wrap to large values
+    return e < (uint32_t)experts ? (int)e : experts;     // `experts`: dropped
+}
+
+// Sums of c[0 .. N) over the workgroup, in every thread.
+template <int N>
+__device__ __forceinline__ void block_counts(uint32_t* c, uint32_t* lds)
+{
+    const int lane = lane_id(), wave = threadIdx.x / kWave, nw = blockDim.x / kWave;
+#pragma unroll
+    for (int j = 0; j < N; ++j)
+        c[j] = wave_sum_u(c[j]);
+    if (nw == 1)
+        return;
+    __syncthreads();   // the previous use of lds is over
+    if (lane == 0)
+#pragma unroll
+        for (int j = 0; j < N; ++j)
+            lds[wave * N + j] = c[j];
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < N; ++j)
+        c[j] = 0;
+    for (int w = 0; w < nw; ++w)
+#pragma unroll
+        for (int j = 0; j < N; ++j)
+            c[j] += lds[w * N + j];
+#pragma unroll
+    for (int j = 0; j < N; ++j)
+        c[j] = (uint32_t)__builtin_amdgcn_readfirstlane((int)c[j]);
+}
+
+// Segment s, expert e: pairs of the segment that go to e, in
+// counts[e * segments + s].
+__global__ __launch_bounds__(256) void k_dispatch_count(DispatchArgs a)
+{
+    __shared__ uint32_t hist[kMaxExperts];
+    for (int e = threadIdx.x; e < a.experts; e += blockDim.x)
+        hist[e] = 0;
+    __syncthreads();
+    const uint32_t lo = blockIdx.x * a.segment;
+    const uint32_t hi = lo + a.segment < a.pairs ? lo + a.segment : a.pairs;
+    for (uint32_t i = lo + threadIdx.x; i < hi; i += blockDim.x) {
+        const int e = local_expert(a.ids[i], a.first, a.experts);
+        if (e < a.experts)
+            atomicAdd(&hist[e], 1u);   // integers: the order does not matter
+    }
+    __syncthreads();
+    for (int e = threadIdx.x; e < a.experts; e += blockDim.x)
+        a.counts[(size_t)e * a.segments + blockIdx.x] = hist[e];
+}
+
+// One expert's counts become the sum of the segments before; its total.
+__global__ __launch_bounds__(256) void k_dispatch_scan(DispatchArgs a)
+{
+    __shared__ uint32_t part[4];
+    uint32_t* c = a.counts + (size_t)blockIdx.x * a.segments;
+    const int lane = lane_id(), wave = threadIdx.x / kWave;
+    uint32_t before = 0;
+    for (uint32_t s0 = 0; s0 < a.segments; s0 += 256) {
+        const uint32_t s = s0 + threadIdx.x;
+        const uint32_t v = s < a.segments ? c[s] : 0;
+        uint32_t incl = v;
+#pragma unroll
+        for (int d = 1; d < kWave; d *= 2) {
+            const uint32_t o = __shfl_up(incl, d);
+            if (lane >= d)
+                incl += o;
+        }
+        __syncthreads();
+        if (lane == kWave - 1)
+            part[wave] = incl;
+        __syncthreads();
+        uint32_t off = before;
+        for (int w = 0; w < wave; ++w)
+            off += part[w];
+        if (s < a.segments)
+            c[s] = off + incl - v;
+        before += part[0] + part[1] + part[2] + part[3];
+    }
+    if (threadIdx.x == 0)
+        a.totals[blockIdx.x] = before;
+}
+
+// OUT 0: the plan alone; 1: rows copied; 2: rows quantized to INT8.
+// SEG: counts come from the two launches above.
+template <int DT, int OUT, bool SEG, bool TAIL>
+__global__ __launch_bounds__(256) void k_dispatch(DispatchArgs a)
+{
+    __shared__ uint32_t lds[4 * (kGroup + 1)];
+    const int tid = threadIdx.x, bd = blockDim.x;
+    const uint32_t t = blockIdx.x;
+
+    if (t >= a.tokens) {
+        // the offsets, kGroup experts a workgroup
+        if (blockIdx.y)
+            return;
+        const int e0 = (int)(t - a.tokens) * kGroup;
+        uint32_t c[kGroup] = {};
+        if constexpr (SEG) {
+            for (int e = tid; e < a.experts; e += bd) {
+                const uint32_t v = a.totals[e];
+#pragma unroll
+                for (int j = 0; j < kGroup; ++j)
+                    c[j] += e < e0 + j ? v : 0;
+            }
+        } else {
+            for (uint32_t i = tid; i < a.pairs; i += bd) {
+                const int e = local_expert(a.ids[i], a.first, a.experts);
+#pragma unroll
+                for (int j = 0; j < kGroup; ++j)
+                    c[j] += e < e0 + j;
+            }
+        }
+        block_counts<kGroup>(c, lds);
+#pragma unroll
+        for (int j = 0; j < kGroup; ++j)
+            if (tid == j && e0 + j <= a.experts)
+                a.offsets[e0 + j] = (int)c[j];
+        return;
+    }
+
+    const void* xrow = static_cast<const char*>(a.x) + (size_t)t * a.ld_x * Elem<DT>::kBytes;
+    constexpr int VE = Elem<DT>::kVE;
+    const int hidden = (int)a.hidden;
+    const int nvec = (hidden + VE - 1) / VE;
+    const int v0 = (int)(blockIdx.y * a.split_vecs);
+    const int v1 = v0 + (int)a.split_vecs < nvec ? v0 + (int)a.split_vecs : nvec;
+
+    float scale = 1.0f, inv = 1.0f;
+    if constexpr (OUT == 2) {
+        uint32_t m = 0;
+        for (int v = tid; v < nvec; v += bd)
+            m = umax(m, vec_absmax<DT>(ld_row<DT, TAIL>(xrow, v, hidden)));
+        m = group_max<kWave>(m);
+        if (bd > kWave) {
+            if (lane_id() == 0)
+                lds[tid / kWave] = m;
+            __syncthreads();
+            for (int w = 0; w < bd / kWave; ++w)
+                m = umax(m, lds[w]);
+        }
+        i8_scale(bits_f32(m), scale, inv);
+    }
+
+    uint32_t kept = 0;
+    for (int j0 = 0; j0 < a.topk; j0 += kGroup) {
+        const int nj = a.topk - j0 < kGroup ? a.topk - j0 : kGroup;
+        const uint32_t i0 = t * (uint32_t)a.topk + (uint32_t)j0;
+        int key[kGroup];
+#pragma unroll
+        for (int j = 0; j < kGroup; ++j)
+            key[j] = j < nj ? local_expert(a.ids[i0 + j], a.first, a.experts) : a.experts;
+        uint32_t c[kGroup + 1] = {};
+        if constexpr (SEG) {
+            const uint32_t seg = i0 / a.segment;   // the token's pairs lie in one segment
+            for (uint32_t i = seg * a.segment + tid; i < i0 + nj; i += bd) {
+                const int e = local_expert(a.ids[i], a.first, a.experts);
+#pragma unroll
+                for (int j = 0; j < kGroup; ++j)
+                    c[j] += e == key[j] && i < i0 + j;
+            }
+            for (int e = tid; e < a.experts; e += bd) {
+                const uint32_t v = a.totals[e];
+                c[kGroup] += v;
+#pragma unroll
+                for (int j = 0; j < kGroup; ++j)
+                    c[j] += e < key[j] ? v : 0;
+            }
+#pragma unroll
+            for (int j = 0; j < kGroup; ++j)
+                if (tid == j && key[j] < a.experts)
+                    c[j] += a.counts[(size_t)key[j] * a.segments + seg];
+        } else {
+            for (uint32_t i = tid; i < a.pairs; i += bd) {
+                const int e = local_expert(a.ids[i], a.first, a.experts);
+                c[kGroup] += e < a.experts;
+#pragma unroll
+                for (int j = 0; j < kGroup; ++j)
+                    c[j] += e < key[j] || (e == key[j] && i < i0 + j);
+            }
+        }
+        block_counts<kGroup + 1>(c, lds);
+        kept = c[kGroup];
+        if (blockIdx.y == 0) {
+#pragma unroll
+            for (int j = 0; j < kGroup; ++j)
+                if (tid == j && j < nj) {
+                    const bool here = key[j] < a.experts;
+                    a.slots[i0 + j] = here ? (int)c[j] : -1;
+                    if (here)
+                        a.order[c[j]] = (int)(i0 + j);
+                }
+        }
+        if constexpr (OUT != 0) {
+            for (int v = v0 + tid; v < v1; v += bd) {
+                const u32x4 x = ld_row<DT, TAIL>(xrow, v, hidden);
+                if constexpr (OUT == 1) {
+#pragma unroll
+                    for (int j = 0; j < kGroup; ++j)
+                        if (key[j] < a.experts)
+                            st_row<DT, TAIL>(static_cast<char*>(a.rows) + (size_t)c[j] * a.ld_rows * Elem<DT>::kBytes,
+                                             v, hidden, x);
+                } else {
+                    uint32_t q[2];
+                    i8_codes<DT>(x, inv, q);
+#pragma unroll
+                    for (int j = 0; j < kGroup; ++j)
+                        if (key[j] < a.experts)
+                            st_codes<DT, TAIL>(static_cast<char*>(a.rows) + (size_t)c[j] * a.ld_rows, v, hidden, q);
+                }
+            }
+            if constexpr (OUT == 2) {
+                if (blockIdx.y == 0)
+#pragma unroll
+                    for (int j = 0; j < kGroup; ++j)
+                        if (tid == j && key[j] < a.experts)
+                            a.row_scales[c[j]] = scale;
+            }
+        }
+    }
+
+    // the rows that no pair owns, spread over the tokens' workgroups
+    for (uint32_t p = kept + t; p < a.pairs; p += a.tokens) {
+        if (tid == 0 && blockIdx.y == 0) {
+            a.order[p] = -1;
+            if constexpr (OUT == 2)
+                a.row_scales[p] = 1.0f;
+        }
+        if constexpr (OUT == 1) {
+            const u32x4 zero = {0, 0, 0, 0};
+            for (int v = v0 + tid; v < v1; v += bd)
+                st_row<DT, TAIL>(static_cast<char*>(a.rows) + (size_t)p * a.ld_rows * Elem<DT>::kBytes, v, hidden,
+                                 zero);
+        }
+        if constexpr (OUT == 2) {
+            const uint32_t zero[2] = {0, 0};
+            for (int v = v0 + tid; v < v1; v += bd)
+                st_codes<DT, TAIL>(static_cast<char*>(a.rows) + (size_t)p * a.ld_rows, v, hidden, zero);
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// combine: a wave holds U x 64 vectors of one token's output
+// ---------------------------------------------------------------------------
+
+// Adds w_j rows[slot_j] for the N lowest set bits of `mask` (lane j holds
+// slot j and weight j); all N rows' loads go out before the first addition.
+template <int DT, bool TAIL, int U, int N>
+__device__ __forceinline__ void combine_batch(const CombineArgs& a, uint64_t& mask, int slot, float w, int v, int hidden,
+                                              float (*acc)[8])
+{
+    constexpr int VE = Elem<DT>::kVE;
+    u32x4 x[N][U];
+    float ws[N];
+#pragma unroll
+    for (int r = 0; r < N; ++r) {
+        const int j = __builtin_ctzll(mask);
+        mask &= mask - 1;
+        const uint32_t s = (uint32_t)__builtin_amdgcn_readlane(slot, j);
+        ws[r] = bits_f32((uint32_t)__builtin_amdgcn_readlane(__builtin_bit_cast(int, w), j));
+        const char* row = static_cast<const char*>(a.rows) + (size_t)s * a.ld_rows * Elem<DT>::kBytes;
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            x[r][u] = ld_row<DT, TAIL, true>(row, v + u * kWave, hidden);
+    }
+#pragma unroll
+    for (int r = 0; r < N; ++r)
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            float f[VE];
+            unpack<DT>(x[r][u], f);
+#pragma unroll
+            for (int k = 0; k < VE; ++k)
+                acc[u][k] += ws[r] * f[k];
+        }
+}
+
+template <int DT, bool TAIL, int U>
+__global__ __launch_bounds__(256) void k_combine(CombineArgs a)
+{
+    const int lane = lane_id();
+    const size_t unit = (size_t)blockIdx.x * (blockDim.x / kWave) +
+                        (uint32_t)__builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    if (unit >= a.tokens * a.chunks)
+        return;
+    const size_t t = unit / a.chunks;
+    const int hidden = (int)a.hidden;
+    const int v = (int)(unit - t * a.chunks) * U * kWave + lane;
+    int slot = -1;
+    float w = 1.0f;
+    if (lane < a.topk) {
+        slot = a.slots[t * a.topk + lane];
+        if (a.weights)
+            w = a.weights[t * a.topk + lane];
+    }
+    uint64_t mask = __ballot((uint32_t)slot < a.nrows);   // a negative slot is large as unsigned
+    float acc[U][8] = {};
+    while (mask) {
+        switch (__builtin_popcountll(mask)) {
+        case 1: combine_batch<DT, TAIL, U, 1>(a, mask, slot, w, v, hidden, acc); break;
+        case 2: combine_batch<DT, TAIL, U, 2>(a, mask, slot, w, v, hidden, acc); break;
+        case 3: combine_batch<DT, TAIL, U, 3>(a, mask, slot, w, v, hidden, acc); break;
+        default: combine_batch<DT, TAIL, U, 4>(a, mask, slot, w, v, hidden, acc); break;
+        }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+        st_row<DT, TAIL, true>(static_cast<char*>(a.out) + t * a.ld_out * Elem<DT>::kBytes, v + u * kWave, hidden,
+                               pack<DT>(acc[u]));
+}
+
+// ---------------------------------------------------------------------------
+// combine's gradient: a workgroup holds one token's d_out, NV vectors a
+// thread at a time, and runs over the token's rows
+// ---------------------------------------------------------------------------
+
+template <int DT, bool TAIL, int NV, bool DW>
+__global__ __launch_bounds__(256) void k_combine_backward(CombineBwdArgs a)
+{
+    constexpr int VE = Elem<DT>::kVE;
+    __shared__ float part[4 * kGroup];
+    const int tid = threadIdx.x, bd = blockDim.x, lane = lane_id(), wave = tid / kWave, nw = bd / kWave;
+    const size_t t = blockIdx.x;
+    const int hidden = (int)a.hidden;
+    const int nvec = (hidden + VE - 1) / VE;
+    const void* grow = static_cast<const char*>(a.d_out) + t * a.ld_d_out * Elem<DT>::kBytes;
+    for (int j0 = 0; j0 < a.topk; j0 += kGroup) {
+        const int nj = a.topk - j0 < kGroup ? a.topk - j0 : kGroup;
+        float dot[kGroup] = {};
+        for (int base = tid; base < nvec; base += bd * NV) {
+            float g[NV][VE];
+#pragma unroll
+            for (int u = 0; u < NV; ++u)
+                unpack<DT>(ld_row<DT, TAIL>(grow, base + u * bd, hidden), g[u]);
+#pragma unroll
+            for (int j = 0; j < kGroup; ++j) {
+                const uint32_t s = j < nj ? (uint32_t)a.slots[t * a.topk + j0 + j] : ~0u;
+                if (s >= a.nrows)
+                    continue;
+                const float w = a.weights ? a.weights[t * a.topk + j0 + j] : 1.0f;
+                if constexpr (DW) {
+                    const char* row = static_cast<const char*>(a.rows) + (size_t)s * a.ld_rows * Elem<DT>::kBytes;
+                    u32x4 x[NV];
+#pragma unroll
+                    for (int u = 0; u < NV; ++u)
+                        x[u] = ld_row<DT, TAIL, true>(row, base + u * bd, hidden);
+#pragma unroll
+                    for (int u = 0; u < NV; ++u) {
+                        float f[VE];
+                        unpack<DT>(x[u], f);
+#pragma unroll
+                        for (int k = 0; k < VE; ++k)
+                            dot[j] += g[u][k] * f[k];
+                    }
+                }
+                char* drow = static_cast<char*>(a.d_rows) + (size_t)s * a.ld_d_rows * Elem<DT>::kBytes;
+#pragma unroll
+                for (int u = 0; u < NV; ++u) {
+                    float f[VE];
+#pragma unroll
+                    for (int k = 0; k < VE; ++k)
+                        f[k] = w * g[u][k];
+                    st_row<DT, TAIL, true>(drow, base + u * bd, hidden, pack<DT>(f));
+                }
+            }
+        }
+        if constexpr (DW) {
+#pragma unroll
+            for (int j = 0; j < kGroup; ++j)
+                dot[j] = wave_sum(dot[j]);
+            __syncthreads();
+            if (lane == 0)
+#pragma unroll
+                for (int j = 0; j < kGroup; ++j)
+                    part[wave * kGroup + j] = dot[j];
+            __syncthreads();
+            if (tid < nj) {
+                float sum = 0.0f;   // a dropped pair's sum has no terms
+                for (int w = 0; w < nw; ++w)
+                    sum += part[w * kGroup + tid];
+                a.d_weights[t * a.topk + j0 + tid] = sum;
+            }
+        }
+    }
+    const u32x4 zero = {0, 0, 0, 0};
+    const int kept = *a.kept < 0 ? 0 : *a.kept;
+    for (size_t p = (size_t)kept + t; p < a.nrows; p += a.tokens)
+        for (int v = tid; v < nvec; v += bd)
+            st_row<DT, TAIL, true>(static_cast<char*>(a.d_rows) + p * a.ld_d_rows * Elem<DT>::kBytes, v, hidden, zero);
+}
+
+template <int OUT, bool SEG>
+const void* dispatch_fn(int dtype, bool tail)
+{
+    if (dtype == 0)
+        return tail ? (const void*)k_dispatch<0, OUT, SEG, true> : (const void*)k_dispatch<0, OUT, SEG, false>;
+    return tail ? (const void*)k_dispatch<1, OUT, SEG, true> : (const void*)k_dispatch<1, OUT, SEG, false>;
+}
+
+template <int U>
+const void* combine_fn(int dtype, bool tail)
+{
+    if (dtype == 0)
+        return tail ? (const void*)k_combine<0, true, U> : (const void*)k_combine<0, false, U>;
+    return tail ? (const void*)k_combine<1, true, U> : (const void*)k_combine<1, false, U>;
+}
+
+template <int NV, bool DW>
+const void* backward_fn(int dtype, bool tail)
+{
+    if (dtype == 0)
+        return tail ? (const void*)k_combine_backward<0, true, NV, DW> : (const void*)k_combine_backward<0, false, NV, DW>;
+    return tail ? (const void*)k_combine_backward<1, true, NV, DW> : (const void*)k_combine_backward<1, false, NV, DW>;
+}
+
+}  // namespace
+
+uint32_t dispatch_segment(int topk) { return (uint32_t)(kSegment / topk * topk); }
+
+hipError_t launch_dispatch(const DispatchArgs& in, int dtype, int out, hipStream_t s)
+{
+    DispatchArgs a = in;
+    void* params[] = {&a};
+    const bool seg = a.pairs > kDispatchCountAll;
+    if (seg) {
+        hipError_t e = launch_logged("k_dispatch_count", (const void*)k_dispatch_count, dim3(a.segments), dim3(256),
+                                     params, s);
+        if (e == hipSuccess)
+            e = launch_logged("k_dispatch_scan", (const void*)k_dispatch_scan, dim3((unsigned)a.experts), dim3(256),
+                              params, s);
+        if (e != hipSuccess)
+            return e;
+    }
+    const size_t nvec = out ? vectors(a.hidden, dtype) : 0;
+    const unsigned wg = out ? threads_for(nvec, 256) : 64u;
+    // enough workgroups to reach every CU when there are few tokens: rows
+    // split into parts of at least one vector a thread
+    size_t splits = 1;
+    if (out && a.tokens) {
+        const size_t want = 2 * (size_t)device_cu_count() / a.tokens;
+        const size_t most = (nvec + wg - 1) / wg;
+        splits = want < 1 ? 1 : want < most ? want : most;
+        if (splits < 1)
+            splits = 1;
+    }
+    a.split_vecs = (uint32_t)((nvec + splits - 1) / splits);
+    const bool tail = out && partial(a.hidden, dtype);
+    const void* fn;
+    if (seg)
+        fn = out == 0 ? dispatch_fn<0, true>(dtype, tail) : out == 1 ? dispatch_fn<1, true>(dtype, tail)
+                                                                     : dispatch_fn<2, true>(dtype, tail);
+    else
+        fn = out == 0 ? dispatch_fn<0, false>(dtype, tail) : out == 1 ? dispatch_fn<1, false>(dtype, tail)
+                                                                      : dispatch_fn<2, false>(dtype, tail);
+    const unsigned offset_wgs = (unsigned)(a.experts / kGroup + 1);   // experts + 1 offsets
+    return launch_logged("k_dispatch", fn, dim3(a.tokens + offset_wgs, (unsigned)splits), dim3(wg), params, s);
+}
+
+hipError_t launch_combine(const CombineArgs& in, int dtype, hipStream_t s)
+{
+    CombineArgs a = in;
+    void* params[] = {&a};
+    const size_t nvec = vectors(a.hidden, dtype);
+    const bool wide = a.tokens * nvec >= (size_t)device_cu_count() * 4096;
+    const int u = wide ? 2 : 1;
+    a.chunks = (nvec + (size_t)u * kWave - 1) / ((size_t)u * kWave);
+    const size_t units = a.tokens * a.chunks;
+    const unsigned wg = wide ? 256u : 64u;
+    const size_t grid = (units * kWave + wg - 1) / wg;
+    const void* fn = wide ? combine_fn<2>(dtype, partial(a.hidden, dtype)) : combine_fn<1>(dtype, partial(a.hidden, dtype));
+    return launch_logged("k_combine", fn, dim3((unsigned)grid), dim3(wg), params, s);
+}
+
+hipError_t launch_combine_backward(const CombineBwdArgs& in, int dtype, hipStream_t s)
+{
+    CombineBwdArgs a = in;
+    void* params[] = {&a};
+    const size_t nvec = vectors(a.hidden, dtype);
+    const bool tail = partial(a.hidden, dtype);
+    const unsigned wg = threads_for(nvec, 256);
+    const bool two = nvec > wg;
+    const void* fn;
+    if (a.d_weights)
+        fn = two ? backward_fn<2, true>(dtype, tail) : backward_fn<1, true>(dtype, tail);
+    else
+        fn = two ? backward_fn<2, false>(dtype, tail) : backward_fn<1, false>(dtype, tail);
+    return launch_logged("k_combine_backward", fn, dim3((unsigned)a.tokens), dim3(wg), params, s);
+}
+
+}  // namespace rx

@@ -9,6 +9,9 @@
 namespace rx {
 
 constexpr int kMaxSrc = 16;
+constexpr int kMaxExperts = 1024;
+constexpr int kMaxTopk = 64;
+constexpr int kMaxNormHidden = 32768;
 
 // Kernel arguments are passed by value, so the pointer tables travel in the
 // kernarg segment and the caller's host arrays can be freed on return.
@@ -58,6 +61,111 @@ struct AllreduceLpArgs {
 // (cached per device on first use).
 int device_cu_count();
 
+struct DispatchArgs {
+    const int* ids;              // tokens x topk
+    int* offsets;                // experts + 1
+    int* order;                  // pairs
+    int* slots;                  // pairs
+    const void* x;
+    void* rows;
+    float* row_scales;
+    uint32_t* counts;            // workspace: experts x segments
+    uint32_t* totals;            // workspace: experts
+    size_t ld_x, ld_rows;        // elements
+    size_t hidden;
+    uint32_t tokens, pairs;
+    uint32_t segment, segments;  // pairs of a counting segment (whole tokens), their number
+    uint32_t split_vecs;         // vectors of a row one workgroup handles
+    int topk, first, experts;
+};
+
+// Up to this many pairs every token's workgroup counts over all of them in
+// the one launch; above, segments are counted first (moe.hip).
+constexpr size_t kDispatchCountAll = 4096;
+
+struct CombineArgs {
+    const void* rows;
+    const int* slots;
+    const float* weights;        // NULL: ones
+    void* out;
+    size_t ld_rows, ld_out, nrows, tokens, hidden;
+    size_t chunks;               // wave units of one token
+    int topk;
+};
+
+struct CombineBwdArgs {
+    const void* d_out;
+    const void* rows;
+    const int* slots;
+    const float* weights;        // NULL: ones
+    const int* kept;
+    void* d_rows;
+    float* d_weights;            // NULL: not wanted
+    size_t ld_d_out, ld_rows, ld_d_rows, nrows, tokens, hidden;
+    int topk;
+};
+
+struct NormArgs {
+    const void* src[kMaxSrc];
+    const void* residual;
+    const void* gate;
+    const void* w_post;
+    const void* w_pre;
+    void* out_h;
+    void* out_z;
+    float* rstd_post;
+    float* rstd_pre;
+    size_t ld_src, ld_residual, ld_h, ld_z;
+    size_t rows, hidden, gate_rows;
+    float residual_scale, eps, inv_hidden;
+    int nsrc;
+};
+
+struct NormBwdArgs {
+    const void* src[kMaxSrc];
+    const void* residual;
+    const void* gate;
+    const void* w_post;
+    const void* w_pre;
+    const float* rstd_post;
+    const float* rstd_pre;
+    const void* d_h;
+    const void* d_z;
+    void* d_src;
+    void* d_residual;
+    float* d_gate;
+    float* d_w_post;
+    float* d_w_pre;
+    float* part_post;            // workspace: parts x hidden
+    float* part_pre;             // workspace: parts x hidden
+    float* part_gate;            // workspace: parts x 2 x hidden
+    size_t ld_src, ld_residual, ld_d_h, ld_d_z, ld_d_src, ld_d_residual;
+    size_t rows, hidden, gate_rows;
+    size_t part_rows;            // rows of one workgroup
+    size_t parts;                // workgroups
+    float residual_scale, inv_hidden;
+    int nsrc;
+};
+
+struct QuantI8Args {
+    const void* x;
+    void* codes;
+    float* scales;
+    size_t ld_x, ld_codes, rows, k;
+};
+
+struct GemmI8Args {
+    const int8_t* a;
+    const int8_t* b;
+    const float* a_scales;
+    const float* b_scales;
+    const int* offsets;          // NULL: one matrix for all rows
+    void* out;
+    size_t ld_a, ld_b, stride_b, ld_out;
+    uint32_t rows, n, k;
+    int experts;
+};
+
 // How a kernel spreads `threads` work items (one per 16-byte vector, or 64
 // per wave tile) over the GPU. Decode-size jobs (`small`) get one work item
 // per thread in `wg_small`-thread workgroups, so that even a 512 KiB message
@@ -96,5 +204,18 @@ hipError_t launch_drr(const DrrArgs& a, int nsrc, int fmt, bool requant, hipStre
 bool allreduce_lp_fits(int dtype, int block);
 hipError_t launch_allreduce_lp(const AllreduceLpArgs& a, int nsrc, int dtype, int fmt, int block,
                                hipStream_t s);
+
+
+// The operators around a block's allreduce.
+uint32_t dispatch_segment(int topk);
+// out: 0 the plan alone, 1 rows copied, 2 rows quantized to INT8
+hipError_t launch_dispatch(const DispatchArgs& a, int dtype, int out, hipStream_t s);
+hipError_t launch_combine(const CombineArgs& a, int dtype, hipStream_t s);
+hipError_t launch_combine_backward(const CombineBwdArgs& a, int dtype, hipStream_t s);
+hipError_t launch_norm(const NormArgs& a, int dtype, hipStream_t s);
+void norm_backward_parts(size_t rows, size_t gate_rows, size_t* part_rows, size_t* parts);
+hipError_t launch_norm_backward(const NormBwdArgs& a, int dtype, hipStream_t s);
+hipError_t launch_quant_i8(const QuantI8Args& a, int dtype, hipStream_t s);
+hipError_t launch_gemm_i8(const GemmI8Args& a, int out_dtype, hipStream_t s);
 
 }  // namespace rx

@@ -51,7 +51,8 @@ typedef enum {
     RX_FP32 = 0,     /* IEEE binary32                                        */
     RX_BF16 = 1,     /* bfloat16                                             */
     RX_FP8_E4M3 = 2, /* OCP E4M3 (E4M3FN): bias 7, max 448, no Inf           */
-    RX_FP8_E5M2 = 3  /* OCP E5M2: bias 15, max 57344                         */
+    RX_FP8_E5M2 = 3, /* OCP E5M2: bias 15, max 57344                         */
+    RX_INT8 = 4      /* two's complement, codes -127 .. 127                  */
 } rx_dtype_t;
 
 typedef enum {
@@ -304,6 +305,198 @@ rx_status_t rx_allreduce_local_noalloc(void* const* bufs, int nsrc, size_t count
  * (codes and scales of every rank, each array 256-B aligned); 0 on invalid
  * arguments. No HIP call. */
 size_t rx_allreduce_local_workspace(int nsrc, size_t count, int block);
+
+/*
+ * ---------------------------------------------------------------------------
+ * The rank-local work of a mixture-of-experts block around its allreduce:
+ * tokens to the experts' rows, the experts' products in 8-bit integers, the
+ * rows back at their tokens, and the sum over the ranks fused with the norms,
+ * the gate and the residual around it.
+ *
+ * Conventions of these entry points, where they differ from the above:
+ *   - Matrices are rows of `hidden` (or k, n) elements, `ld` elements apart
+ *     (ld >= the row's length, any value; 64-bit offsets). Pointers need the
+ *     alignment of their element only, unless stated; rows that start 16-byte
+ *     aligned are as fast as the memory, others somewhat slower.
+ *   - Elements between the rows' ends and the next row are neither read (but
+ *     see rx_gemm_i8) nor written.
+ *   - Outputs must not overlap inputs or each other except where stated.
+ *   - Pointers to data without elements may be NULL.
+ *   - rows, tokens < 2^22; the number of threads of one launch is limited.
+ *   - Results do not depend on timing: no floating-point sum is formed in an
+ *     order that could change between two calls.
+ * ---------------------------------------------------------------------------
+ */
+
+#define RX_MAX_TOPK 64
+#define RX_MAX_EXPERTS 1024
+
+/*
+ * Tokens sorted by expert. Pair i = t topk + j is token t's j-th choice; it
+ * belongs here when first_expert <= expert_ids[i] < first_expert + experts,
+ * otherwise (another rank's expert, or a negative id) it is dropped.
+ *   offsets[e]  pairs of experts 0 .. e-1 (local numbers); offsets[experts]
+ *               is the number kept; experts + 1 values.
+ *   order[p]    the pair in sorted row p (by expert, then by i), -1 for
+ *               p >= offsets[experts]; tokens topk values.
+ *   slots[i]    the sorted row of pair i, -1 when it is dropped.
+ *   rows[p, :]  = x[order[p] / topk, :] for kept rows, 0 for the others
+ *               (tokens topk rows). rows_dtype is x_dtype, or RX_INT8: then
+ *               each token is quantized as rx_quant_i8 does and row_scales[p]
+ *               receives its scale (1 for the rows past offsets[experts]).
+ * x == NULL (with rows and row_scales NULL) computes the plan alone. The
+ * gather's gradient with respect to x is rx_moe_combine of d_rows with
+ * weights == NULL.
+ *
+ * tokens topk < 2^31; topk 1 .. RX_MAX_TOPK; experts 1 .. RX_MAX_EXPERTS;
+ * first_expert >= 0. workspace: rx_moe_dispatch_workspace() bytes, 4-byte
+ * aligned (NULL where that is 0); its contents on return are unspecified.
+ */
+rx_status_t rx_moe_dispatch(const int* expert_ids, size_t tokens, int topk,
+                            int first_expert, int experts, const void* x,
+                            size_t ld_x, size_t hidden, rx_dtype_t x_dtype,
+                            int* offsets, int* order, int* slots, void* rows,
+                            size_t ld_rows, rx_dtype_t rows_dtype,
+                            float* row_scales, void* workspace,
+                            size_t workspace_bytes, hipStream_t stream);
+
+/* Workspace bytes of rx_moe_dispatch; 0 also on invalid arguments. No HIP call. */
+size_t rx_moe_dispatch_workspace(size_t tokens, int topk, int experts);
+
+/*
+ * Sorted rows back at their tokens, with the router's weights:
+ *   out[t, :] = cast( sum over j, in order, of weights[t, j] rows[slots[t, j], :] )
+ * in FP32, one rounding per product and one per addition. Pairs whose slot is
+ * negative or not below nrows are left out and their rows never read; a token
+ * without pairs gets zeros. weights == NULL: all ones.
+ *
+ * rows, out : RX_FP32 or RX_BF16 (the same); weights: FP32, tokens x topk.
+ */
+rx_status_t rx_moe_combine(const void* rows, size_t ld_rows, size_t nrows,
+                           const int* slots, const float* weights,
+                           size_t tokens, int topk, size_t hidden,
+                           rx_dtype_t dtype, void* out, size_t ld_out,
+                           hipStream_t stream);
+
+/*
+ * Gradient of rx_moe_combine, for slots that rx_moe_dispatch wrote (each row
+ * is owned by at most one pair, kept rows are 0 .. *kept - 1):
+ *   d_rows[slots[t, j], :] = cast( weights[t, j] d_out[t, :] ), 0 for the
+ *                            rows from *kept to nrows
+ *   d_weights[t, j]        = sum over c of d_out[t, c] rows[slots[t, j], c]
+ *                            in FP32, 0 for a dropped pair
+ * kept      : device pointer to the number of kept rows (offsets + experts).
+ * weights   : NULL for ones. d_weights, and rows with it: NULL when the
+ *             weights need no gradient.
+ */
+rx_status_t rx_moe_combine_backward(const void* d_out, size_t ld_d_out,
+                                    const void* rows, size_t ld_rows, size_t nrows,
+                                    const int* slots, const float* weights,
+                                    const int* kept, size_t tokens, int topk,
+                                    size_t hidden, rx_dtype_t dtype, void* d_rows,
+                                    size_t ld_d_rows, float* d_weights,
+                                    hipStream_t stream);
+
+/*
+ * The sum over the ranks fused with what surrounds it in a block: the norm
+ * after the block, its gate, the scaled residual, and the next block's norm.
+ *   y = (((src_0 + src_1) + ...) + src_{nsrc-1})        FP32, as rx_reduce_flat
+ *   u = y p w_post, p = 1 / sqrt(mean(y^2) + eps)       (w_post NULL: u = y)
+ *   h = residual_scale residual + g u                   (residual NULL: h = g u)
+ *   z = h q w_pre,  q = 1 / sqrt(mean(h^2) + eps)
+ * for every row, in FP32 from the inputs to the one rounding of each output:
+ * z is formed from the unrounded h. Row t uses row t / gate_rows of gate
+ * (ceil(rows / gate_rows) rows of `hidden`, packed; gate NULL: g = 1).
+ *
+ * srcs, residual, gate, w_post, w_pre, out_h, out_z: dtype (RX_FP32 or RX_BF16).
+ * out_h, out_z        : either may be NULL; w_pre may be NULL when out_z is.
+ *                       out_h may equal residual or one srcs[j] exactly
+ *                       (same ld).
+ * rstd_post, rstd_pre : NULL, or `rows` floats each that receive p and q for
+ *                       the backward pass (p only when w_post is given, q
+ *                       only when out_z is).
+ * eps                 : positive and finite.
+ * A row that is all zero gives u = 0 (or z = 0).
+ */
+rx_status_t rx_residual_norm(const void* const* srcs, int nsrc, size_t ld_src,
+                             const void* residual, size_t ld_residual,
+                             const void* gate, size_t gate_rows,
+                             const void* w_post, const void* w_pre,
+                             float residual_scale, float eps, size_t rows,
+                             size_t hidden, rx_dtype_t dtype, void* out_h,
+                             size_t ld_h, void* out_z, size_t ld_z,
+                             float* rstd_post, float* rstd_pre,
+                             hipStream_t stream);
+
+/*
+ * Gradient of rx_residual_norm from d_h and d_z, the gradients of its two
+ * outputs (either may be NULL: zero), the forward call's inputs and the p and
+ * q that it wrote (rstd_pre is needed with d_z, rstd_post with w_post). With
+ * a = d_z w_pre, b = d_u w_post and means over the row:
+ *   dH         = d_h + q (a - h q^2 mean(a h))
+ *   d_residual = residual_scale dH
+ *   d_u        = g dH
+ *   d_src      = p (b - y p^2 mean(b y))      (w_post NULL: d_u); the gradient
+ *                                             of every one of the sources
+ *   d_gate     = sum over the gate's rows of dH u
+ *   d_w_post   = sum over rows of d_u y p
+ *   d_w_pre    = sum over rows of d_z h q
+ * d_src and d_residual: dtype, rows of `hidden`; d_residual may be NULL (and
+ * must be with residual NULL), and may equal d_h exactly. d_gate, d_w_post
+ * and d_w_pre: FP32, packed, each NULL when it is not wanted or its operand
+ * is absent.
+ * workspace: rx_residual_norm_backward_workspace() bytes, 16-byte aligned.
+ */
+rx_status_t rx_residual_norm_backward(const void* const* srcs, int nsrc, size_t ld_src,
+                                      const void* residual, size_t ld_residual,
+                                      const void* gate, size_t gate_rows,
+                                      const void* w_post, const void* w_pre,
+                                      const float* rstd_post, const float* rstd_pre,
+                                      float residual_scale, size_t rows, size_t hidden,
+                                      rx_dtype_t dtype, const void* d_h, size_t ld_d_h,
+                                      const void* d_z, size_t ld_d_z, void* d_src,
+                                      size_t ld_d_src, void* d_residual,
+                                      size_t ld_d_residual, float* d_gate,
+                                      float* d_w_post, float* d_w_pre, void* workspace,
+                                      size_t workspace_bytes, hipStream_t stream);
+
+/* Workspace bytes of rx_residual_norm_backward for any of its optional
+ * operands; 0 on invalid arguments. Looks up the device's compute-unit count. */
+size_t rx_residual_norm_backward_workspace(size_t rows, size_t hidden, size_t gate_rows);
+
+/*
+ * Rows to 8-bit integers with one FP32 scale a row:
+ *   A = max |x| over the row, s = A / 127, r = 127 / A (each the correctly
+ *   rounded FP32 quotient; A == 0, s == 0 or r not finite: s = r = 1),
+ *   code = the integer nearest to fl32(x r), ties to even, within -127 .. 127.
+ * x: RX_FP32 or RX_BF16, rows of k elements; codes: ld_codes bytes apart.
+ */
+rx_status_t rx_quant_i8(const void* x, size_t ld_x, size_t rows, size_t k,
+                        rx_dtype_t dtype, void* codes, size_t ld_codes,
+                        float* scales, hipStream_t stream);
+
+/*
+ * Product of 8-bit integer matrices with a scale for each token (row of a)
+ * and each channel (row of b):
+ *   out[m, j] = cast( fl32( fl32(sum over i of a[m, i] b[j, i]) a_scales[m] ) b_scales[j] )
+ * with the sum exact in INT32. offsets == NULL: one matrix b of n rows,
+ * experts == 1. Otherwise (rx_moe_dispatch's offsets, experts + 1 values on
+ * the device, never decreasing) rows offsets[e] .. offsets[e+1] - 1 are
+ * multiplied with b's matrix e (n rows each, b + e stride_b; b_scales + e n),
+ * and the rows past offsets[experts] become 0.
+ *
+ * a, b       : INT8; pointers 16-byte aligned; ld_a, ld_b (and stride_b)
+ *              multiples of 16, at least k rounded up to 16. The bytes from k
+ *              to that multiple are read and may hold anything.
+ * k          : up to 131071 (the exact sum fits 32 bits); k == 0 gives zeros.
+ * out        : RX_FP32 or RX_BF16.
+ * rows < 2^31, n < 2^31. Offsets outside 0 .. rows are clamped to that range.
+ */
+rx_status_t rx_gemm_i8(const void* a, size_t ld_a, const float* a_scales,
+                       const void* b, size_t ld_b, size_t stride_b,
+                       const float* b_scales, const int* offsets, int experts,
+                       size_t rows, size_t n, size_t k, void* out, size_t ld_out,
+                       rx_dtype_t out_dtype, hipStream_t stream);
 
 /* Static description of a status code (never NULL). */
 const char* rx_status_string(rx_status_t s);

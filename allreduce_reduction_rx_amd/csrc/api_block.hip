@@ -230,9 +230,7 @@ size_t rx_residual_norm_backward_workspace(size_t rows, size_t hidden, size_t ga
 {
     if (rows > kMaxRows || hidden > (size_t)kMaxNormHidden)
         return 0;
-    size_t part_rows, parts;
-    norm_backward_parts(rows, gate_rows_or_one(gate_rows, rows), &part_rows, &parts);
-    return parts * hidden * 4 * sizeof(float);
+    return norm_backward_parts(rows, hidden, gate_rows_or_one(gate_rows, rows)) * hidden * 4 * sizeof(float);
 }
 
 rx_status_t rx_residual_norm_backward(const void* const* srcs, int nsrc, size_t ld_src, const void* residual,
@@ -306,10 +304,7 @@ rx_status_t rx_residual_norm_backward(const void* const* srcs, int nsrc, size_t 
     a.rows = rows;
     a.hidden = hidden;
     a.gate_rows = gate_rows_or_one(gate_rows, rows);
-    norm_backward_parts(rows, a.gate_rows, &a.part_rows, &a.parts);
     a.part_post = static_cast<float*>(workspace);
-    a.part_pre = a.part_post + a.parts * hidden;
-    a.part_gate = a.part_pre + a.parts * hidden;
     a.residual_scale = residual_scale;
     a.inv_hidden = (float)(1.0 / (double)hidden);
     a.nsrc = nsrc;

@@ -36,7 +36,9 @@ __device__ __forceinline__ void st16_any_stream(void* p, u32x4 v)
 
 // Vector v of a row of `hidden` elements. TAIL: the row's last vector may be
 // partial (its missing elements read as 0 and are not written); vectors past
-// the row are 0. Without TAIL hidden is a multiple of the vector.
+// the row are 0. Without TAIL hidden is a multiple of the vector. A row is
+// shorter than 2^32 bytes: with a uniform row pointer the 32-bit offset lets
+// the address stay in scalar registers.
 template <int DT, bool TAIL, bool NT = false>
 __device__ __forceinline__ u32x4 ld_row(const void* row, int v, int hidden)
 {
@@ -45,8 +47,8 @@ __device__ __forceinline__ u32x4 ld_row(const void* row, int v, int hidden)
     u32x4 x = {0, 0, 0, 0};
     if (!TAIL || c + VE <= hidden) {
         if (TAIL || c < hidden)
-            x = NT ? ld16_any_stream(static_cast<const char*>(row) + (size_t)c * Elem<DT>::kBytes)
-                   : ld16_any(static_cast<const char*>(row) + (size_t)c * Elem<DT>::kBytes);
+            x = NT ? ld16_any_stream(static_cast<const char*>(row) + (uint32_t)c * (uint32_t)Elem<DT>::kBytes)
+                   : ld16_any(static_cast<const char*>(row) + (uint32_t)c * (uint32_t)Elem<DT>::kBytes);
     } else if (c < hidden) {
         const int n = hidden - c;   // 1 .. VE - 1
         if constexpr (DT == 0) {
@@ -72,7 +74,7 @@ __device__ __forceinline__ void st_row(void* row, int v, int hidden, u32x4 x)
     const int c = v * VE;
     if (!TAIL || c + VE <= hidden) {
         if (TAIL || c < hidden) {
-            char* p = static_cast<char*>(row) + (size_t)c * Elem<DT>::kBytes;
+            char* p = static_cast<char*>(row) + (uint32_t)c * (uint32_t)Elem<DT>::kBytes;
             if (NT) st16_any_stream(p, x); else st16_any(p, x);
         }
     } else if (c < hidden) {

@@ -136,7 +136,7 @@ struct NormBwdArgs {
     float* d_gate;
     float* d_w_post;
     float* d_w_pre;
-    float* part_post;            // workspace: parts x hidden
+    float* part_post;            // workspace (the launch lays out the parts): parts x hidden
     float* part_pre;             // workspace: parts x hidden
     float* part_gate;            // workspace: parts x 2 x hidden
     size_t ld_src, ld_residual, ld_d_h, ld_d_z, ld_d_src, ld_d_residual;
@@ -213,7 +213,7 @@ hipError_t launch_dispatch(const DispatchArgs& a, int dtype, int out, hipStream_
 hipError_t launch_combine(const CombineArgs& a, int dtype, hipStream_t s);
 hipError_t launch_combine_backward(const CombineBwdArgs& a, int dtype, hipStream_t s);
 hipError_t launch_norm(const NormArgs& a, int dtype, hipStream_t s);
-void norm_backward_parts(size_t rows, size_t gate_rows, size_t* part_rows, size_t* parts);
+size_t norm_backward_parts(size_t rows, size_t hidden, size_t gate_rows);
 hipError_t launch_norm_backward(const NormBwdArgs& a, int dtype, hipStream_t s);
 hipError_t launch_quant_i8(const QuantI8Args& a, int dtype, hipStream_t s);
 hipError_t launch_gemm_i8(const GemmI8Args& a, int out_dtype, hipStream_t s);

@@ -13,6 +13,7 @@ using namespace rx;
 // launch has fewer than 2^32 threads.
 constexpr size_t kMaxRows = ((size_t)1 << 22) - 1;
 constexpr size_t kMaxLd = (size_t)1 << 36;   // row offsets stay far inside 64 bits
+constexpr size_t kMaxGemmLd = (size_t)1 << 23;   // a tile's 256 rows lie within 32 bits
 constexpr size_t kMaxHidden = (size_t)1 << 30;
 
 size_t elem_size(rx_dtype_t t) { return t == RX_BF16 ? 2 : t == RX_INT8 ? 1 : 4; }
@@ -41,9 +42,8 @@ size_t rx_moe_dispatch_workspace(size_t tokens, int topk, int experts)
 {
     if (!dispatch_sizes_ok(tokens, topk, experts) || tokens * (size_t)topk <= kDispatchCountAll)
         return 0;
-    const size_t seg = dispatch_segment(topk);
-    const size_t segments = (tokens * (size_t)topk + seg - 1) / seg;
-    return ((size_t)experts * segments + (size_t)experts) * sizeof(uint32_t);
+    const size_t pairs = tokens * (size_t)topk, seg = dispatch_segment(pairs);
+    return (size_t)experts * ((pairs + seg - 1) / seg) * sizeof(uint32_t);
 }
 
 rx_status_t rx_moe_dispatch(const int* expert_ids, size_t tokens, int topk, int first_expert, int experts,
@@ -93,10 +93,9 @@ rx_status_t rx_moe_dispatch(const int* expert_ids, size_t tokens, int topk, int 
     a.hidden = hidden;
     a.tokens = (uint32_t)tokens;
     a.pairs = (uint32_t)(tokens * (size_t)topk);
-    a.segment = dispatch_segment(topk);
+    a.segment = dispatch_segment(a.pairs);
     a.segments = (a.pairs + a.segment - 1) / a.segment;
     a.counts = static_cast<uint32_t*>(workspace);
-    a.totals = need ? a.counts + (size_t)experts * a.segments : nullptr;
     a.topk = topk;
     a.first = first_expert;
     a.experts = experts;
@@ -343,7 +342,8 @@ rx_status_t rx_gemm_i8(const void* a, size_t ld_a, const float* a_scales, const 
         return RX_ERR_NULL;
     const size_t k16 = (k + 15) / 16 * 16;
     if (rows > kMaxRows || n >= ((size_t)1 << 31) || k > 131071 || experts < 1 || experts > kMaxExperts ||
-        (!offsets && experts != 1) || bad_ld(ld_a, k16) || bad_ld(ld_b, k16) || bad_ld(ld_out, n, rows) ||
+        (!offsets && experts != 1) || (rows > 1 && ld_a >= kMaxGemmLd) ||
+        (n > 1 && ld_b >= kMaxGemmLd) || bad_ld(ld_a, k16) || bad_ld(ld_b, k16) || bad_ld(ld_out, n, rows) ||
         stride_b > kMaxLd * 16)
         return RX_ERR_ARG;
     if (!hp_type(out_dtype))
@@ -351,8 +351,8 @@ rx_status_t rx_gemm_i8(const void* a, size_t ld_a, const float* a_scales, const 
     if (!aligned16(a) || !aligned16(b) || ld_a % 16 || ld_b % 16 || stride_b % 16 || !aligned4(a_scales) ||
         !aligned4(b_scales) || !aligned4(offsets) || !element_aligned(out, out_dtype))
         return RX_ERR_ALIGN;
-    // a workgroup for every 128 x 128 outputs or finer, fewer than 2^24
-    if ((rows / 16 + (size_t)experts + 1) * ((n + 15) / 16) >= ((size_t)1 << 24) * 64)
+    // 256 x 256 outputs of 512 threads, a partial tile for every expert: a launch's limit of 2^32 threads
+    if ((rows / 256 + (size_t)experts + 1) * ((n + 255) / 256) >= ((size_t)1 << 23) - 8)
         return RX_ERR_ARG;
     if (rows == 0 || n == 0)
         return RX_OK;

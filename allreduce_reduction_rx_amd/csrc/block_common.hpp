@@ -165,13 +165,15 @@ __device__ __forceinline__ uint32_t vec_absmax(u32x4 x)
 }
 
 // A row's INT8 scale and multiplier from its absmax A: fl32(A / 127) and
-// fl32(127 / A); 1 where a quotient is useless. Once a row: plain divisions.
+// fl32(127 / A); 1 where a quotient is useless, A and 0 where A is not finite
+// (its products are then NaN). Once a row: plain divisions.
 __device__ __forceinline__ void i8_scale(float a, float& s, float& r)
 {
     const float sv = a / 127.0f, rv = 127.0f / a;
     const bool degenerate = (a == 0.0f) | (sv == 0.0f) | !__builtin_isfinite(rv);
-    s = degenerate ? 1.0f : sv;
-    r = degenerate ? 1.0f : rv;
+    const bool finite = __builtin_isfinite(a);
+    s = !finite ? a : degenerate ? 1.0f : sv;
+    r = !finite ? 0.0f : degenerate ? 1.0f : rv;
 }
 
 // The codes of a vector, 4 a word. |x r| <= 127 (1 + 2^-23), so adding
@@ -191,7 +193,7 @@ __device__ __forceinline__ void i8_codes(u32x4 x, float r, uint32_t* q)
     for (int k = 0; k < VE / 4; ++k) {
         const uint32_t lo = __builtin_amdgcn_perm(b[4 * k + 1], b[4 * k], 0x0C0C0400);      // bytes 0, 0
         const uint32_t hi = __builtin_amdgcn_perm(b[4 * k + 3], b[4 * k + 2], 0x0C0C0400);
-        q[k] = lo | hi << 16;
+        q[k] = r == 0.0f ? 0 : lo | hi << 16;   // a NaN's product may have any low byte
     }
 }
 

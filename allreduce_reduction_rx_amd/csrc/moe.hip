@@ -7,20 +7,20 @@
 // sizes.
 //
 // The sort. The sorted place of pair i is a count: the pairs with a smaller
-// expert, and the pairs before i with the same one. Each token's workgroup
-// counts for its own topk pairs (compares and adds over ids that sit in L2),
-// so no ordering pass writes the order before the gather reads it, the
-// places come out stable, and they do not depend on timing. Up to kCountAll
-// pairs the count runs over all ids in the one launch that gathers. Above,
-// two small launches count experts per segment of kSegment pairs and sum
-// over segments, and a token counts in its own segment only.
+// expert, and the pairs before i with the same one, so the places are stable
+// and do not depend on timing. Up to kDispatchCountAll pairs each token's
+// workgroup counts for its own topk pairs over all ids (compares and adds
+// over ids that sit in L2) in the one launch that gathers. Above, a launch
+// counts experts per segment of pairs, a second one places the pairs of each
+// segment, and the third only moves rows.
 #include "block_common.hpp"
 
 namespace rx {
 namespace {
 
 constexpr int kGroup = 8;          // a token's pairs handled together
-constexpr int kSegment = 1024;     // pairs of a counting segment (rounded down to whole tokens)
+constexpr int kPlace = 1024;       // pairs placed at a time, threads of the kernels that count and place
+constexpr int kSegments = 256;     // at most: a workgroup for every CU
 
 __device__ __forceinline__ int local_expert(int id, int first, int experts)
 {
@@ -57,8 +57,8 @@ __device__ __forceinline__ void block_counts(uint32_t* c, uint32_t* lds)
 }
 
 // Segment s, expert e: pairs of the segment that go to e, in
-// counts[e * segments + s].
-__global__ __launch_bounds__(256) void k_dispatch_count(DispatchArgs a)
+// counts[s * experts + e].
+__global__ __launch_bounds__(kPlace) void k_dispatch_count(DispatchArgs a)
 {
     __shared__ uint32_t hist[kMaxExperts];
     for (int e = threadIdx.x; e < a.experts; e += blockDim.x)
@@ -66,51 +66,210 @@ __global__ __launch_bounds__(256) void k_dispatch_count(DispatchArgs a)
     __syncthreads();
     const uint32_t lo = blockIdx.x * a.segment;
     const uint32_t hi = lo + a.segment < a.pairs ? lo + a.segment : a.pairs;
-    for (uint32_t i = lo + threadIdx.x; i < hi; i += blockDim.x) {
+    for (uint32_t i = lo + threadIdx.x; i < hi; i += kPlace) {
         const int e = local_expert(a.ids[i], a.first, a.experts);
         if (e < a.experts)
             atomicAdd(&hist[e], 1u);   // integers: the order does not matter
     }
     __syncthreads();
     for (int e = threadIdx.x; e < a.experts; e += blockDim.x)
-        a.counts[(size_t)e * a.segments + blockIdx.x] = hist[e];
+        a.counts[(size_t)blockIdx.x * a.experts + e] = hist[e];
 }
 
-// One expert's counts become the sum of the segments before; its total.
-__global__ __launch_bounds__(256) void k_dispatch_scan(DispatchArgs a)
+// The lanes whose key equals this lane's (keys of up to 11 bits).
+__device__ __forceinline__ uint64_t same_key(int key, int bits)
 {
-    __shared__ uint32_t part[4];
-    uint32_t* c = a.counts + (size_t)blockIdx.x * a.segments;
-    const int lane = lane_id(), wave = threadIdx.x / kWave;
-    uint32_t before = 0;
-    for (uint32_t s0 = 0; s0 < a.segments; s0 += 256) {
-        const uint32_t s = s0 + threadIdx.x;
-        const uint32_t v = s < a.segments ? c[s] : 0;
-        uint32_t incl = v;
+    uint64_t same = ~0ull;
+    for (int b = 0; b < bits; ++b) {
+        const uint64_t set = __ballot(key >> b & 1);
+        same &= key >> b & 1 ? set : ~set;
+    }
+    return same;
+}
+
+// Places the pairs of segment blockIdx.x; segment 0 writes the offsets too.
+__global__ __launch_bounds__(kPlace) void k_dispatch_place(DispatchArgs a)
+{
+    constexpr int kWaves = kPlace / kWave;
+    __shared__ uint32_t base[kMaxExperts];               // the next place of each expert
+    __shared__ uint32_t part[2][kPlace];
+    __shared__ uint16_t hist[kWaves][kMaxExperts];
+    __shared__ uint32_t wsum[kWaves];
+    const int tid = threadIdx.x, lane = lane_id(), wave = tid / kWave, experts = a.experts;
+
+    // totals of each expert, and the counts of the segments before: the
+    // segments dealt to the threads of an expert
+    uint32_t width = kWave;
+    while ((int)width < experts)
+        width *= 2;
+    const uint32_t e = tid % width, g = tid / width, groups = kPlace / width;
+    uint32_t total = 0, before = 0;
+    if ((int)e < experts)
+#pragma unroll 8
+        for (uint32_t s = g; s < a.segments; s += groups) {
+            const uint32_t c = a.counts[(size_t)s * experts + e];
+            total += c;
+            before += s < blockIdx.x ? c : 0;
+        }
+    part[0][tid] = total;
+    part[1][tid] = before;
+    for (int i = tid; i < kWaves * kMaxExperts / 2; i += kPlace)
+        reinterpret_cast<uint32_t*>(&hist[0][0])[i] = 0;
+    __syncthreads();
+    total = before = 0;
+    if (g == 0)
+        for (uint32_t i = 0; i < groups; ++i) {
+            total += part[0][i * width + e];
+            before += part[1][i * width + e];
+        }
+    // the experts' starts: an exclusive sum over the workgroup
+    uint32_t incl = total;
 #pragma unroll
-        for (int d = 1; d < kWave; d *= 2) {
-            const uint32_t o = __shfl_up(incl, d);
-            if (lane >= d)
-                incl += o;
+    for (int d = 1; d < kWave; d *= 2) {
+        const uint32_t o = __shfl_up(incl, d);
+        if (lane >= d)
+            incl += o;
+    }
+    if (lane == kWave - 1)
+        wsum[wave] = incl;
+    __syncthreads();
+    uint32_t start = incl - total, kept = 0;
+    for (int w = 0; w < kWaves; ++w) {
+        start += w < wave ? wsum[w] : 0;
+        kept += wsum[w];
+    }
+    if (tid < experts) {
+        base[tid] = start + before;
+        if (blockIdx.x == 0)
+            a.offsets[tid] = (int)start;
+    }
+    if (blockIdx.x == 0 && tid == 0)
+        a.offsets[experts] = (int)kept;
+
+    int bits = 1;
+    while (1 << bits <= experts)   // keys 0 .. experts
+        ++bits;
+    const uint32_t lo = blockIdx.x * a.segment;
+    const uint32_t hi = lo + a.segment < a.pairs ? lo + a.segment : a.pairs;
+    for (uint32_t i0 = lo; i0 < hi; i0 += kPlace) {
+        const uint32_t i = i0 + tid;
+        const int key = i < hi ? local_expert(a.ids[i], a.first, experts) : experts;
+        const uint64_t same = same_key(key, bits);
+        const uint32_t rank = __popcll(same & ((1ull << lane) - 1));
+        const bool owned = key < experts, last = owned && (same >> lane) == 1;   // no higher lane has this key
+        if (last)
+            hist[wave][key] = (uint16_t)(rank + 1);
+        __syncthreads();
+        uint32_t p = 0;
+        if (owned) {
+            p = base[key] + rank;
+            for (int w = 0; w < wave; ++w)
+                p += hist[w][key];
+            a.order[p] = (int)i;
+        }
+        if (i < hi)
+            a.slots[i] = owned ? (int)p : -1;
+        __syncthreads();   // base and hist have been read
+        if (last) {
+            atomicAdd(&base[key], rank + 1);
+            hist[wave][key] = 0;
         }
         __syncthreads();
-        if (lane == kWave - 1)
-            part[wave] = incl;
-        __syncthreads();
-        uint32_t off = before;
-        for (int w = 0; w < wave; ++w)
-            off += part[w];
-        if (s < a.segments)
-            c[s] = off + incl - v;
-        before += part[0] + part[1] + part[2] + part[3];
     }
-    if (threadIdx.x == 0)
-        a.totals[blockIdx.x] = before;
+    for (uint32_t p = (lo < kept ? kept : lo) + tid; p < hi; p += kPlace)
+        a.order[p] = -1;
 }
 
-// OUT 0: the plan alone; 1: rows copied; 2: rows quantized to INT8.
-// SEG: counts come from the two launches above.
-template <int DT, int OUT, bool SEG, bool TAIL>
+// Moves rows to the places in slots. OUT 1: copied; 2: quantized to INT8.
+template <int DT, int OUT, bool TAIL, int NV>
+__global__ __launch_bounds__(256) void k_dispatch_rows(DispatchArgs a)
+{
+    constexpr int VE = Elem<DT>::kVE, EB = OUT == 1 ? Elem<DT>::kBytes : 1;
+    __shared__ uint32_t lds[4];
+    const int tid = threadIdx.x, bd = blockDim.x;
+    const uint32_t t = blockIdx.x;
+    const void* xrow = static_cast<const char*>(a.x) + (size_t)t * a.ld_x * Elem<DT>::kBytes;
+    const int hidden = (int)a.hidden;
+    const int nvec = (hidden + VE - 1) / VE;
+    const int v0 = (int)(blockIdx.y * a.split_vecs);
+    const int v1 = v0 + (int)a.split_vecs < nvec ? v0 + (int)a.split_vecs : nvec;
+    u32x4 x[NV];
+    auto load = [&](int base) {
+#pragma unroll
+        for (int u = 0; u < NV; ++u)
+            x[u] = ld_row<DT, TAIL, OUT == 1>(xrow, base + u * bd, hidden);
+    };
+    load(v0 + tid);
+    float scale = 1.0f, inv = 1.0f;
+    if constexpr (OUT == 2) {
+        uint32_t m = 0;
+#pragma unroll
+        for (int u = 0; u < NV; ++u)
+            m = umax(m, vec_absmax<DT>(x[u]));
+        // what the registers do not hold: the row's other splits, its rest
+        for (int v = tid; v < nvec; v += bd)
+            if (v < v0 || v >= v0 + NV * bd)
+                m = umax(m, vec_absmax<DT>(ld_row<DT, TAIL>(xrow, v, hidden)));
+        m = group_max<kWave>(m);
+        if (bd > kWave) {
+            if (lane_id() == 0)
+                lds[tid / kWave] = m;
+            __syncthreads();
+            for (int w = 0; w < bd / kWave; ++w)
+                m = umax(m, lds[w]);
+        }
+        i8_scale(bits_f32(m), scale, inv);
+        if (blockIdx.y == 0)
+            for (int j = tid; j < a.topk; j += bd) {
+                const int s = a.slots[(size_t)t * a.topk + j];
+                if (s >= 0)
+                    a.row_scales[s] = scale;
+            }
+    }
+    for (int base = v0 + tid; base - tid < v1; base += NV * bd) {
+        if (base - tid > v0)
+            load(base);
+        uint32_t q[NV][2];
+        if constexpr (OUT == 2)
+#pragma unroll
+            for (int u = 0; u < NV; ++u)
+                i8_codes<DT>(x[u], inv, q[u]);
+        for (int j = 0; j < a.topk; ++j) {
+            const int s = a.slots[(size_t)t * a.topk + j];
+            if (s < 0)
+                continue;
+            char* row = static_cast<char*>(a.rows) + (size_t)s * a.ld_rows * EB;
+#pragma unroll
+            for (int u = 0; u < NV; ++u) {
+                const int v = base + u * bd;
+                if (v >= v1)
+                    continue;
+                if constexpr (OUT == 1)
+                    st_row<DT, TAIL, true>(row, v, hidden, x[u]);
+                else
+                    st_codes<DT, TAIL>(row, v, hidden, q[u]);
+            }
+        }
+    }
+    // the rows that no pair owns, spread over the tokens' workgroups
+    for (uint32_t p = (uint32_t)a.offsets[a.experts] + t; p < a.pairs; p += a.tokens) {
+        char* row = static_cast<char*>(a.rows) + (size_t)p * a.ld_rows * EB;
+        const u32x4 zero = {0, 0, 0, 0};
+        const uint32_t none[2] = {0, 0};
+        if (OUT == 2 && tid == 0 && blockIdx.y == 0)
+            a.row_scales[p] = 1.0f;
+        for (int v = v0 + tid; v < v1; v += bd) {
+            if constexpr (OUT == 1)
+                st_row<DT, TAIL, true>(row, v, hidden, zero);
+            else
+                st_codes<DT, TAIL>(row, v, hidden, none);
+        }
+    }
+}
+
+// Plan and rows in one launch. OUT 0: the plan alone; 1: rows copied; 2: rows
+// quantized to INT8.
+template <int DT, int OUT, bool TAIL>
 __global__ __launch_bounds__(256) void k_dispatch(DispatchArgs a)
 {
     __shared__ uint32_t lds[4 * (kGroup + 1)];
@@ -123,20 +282,11 @@ __global__ __launch_bounds__(256) void k_dispatch(DispatchArgs a)
             return;
         const int e0 = (int)(t - a.tokens) * kGroup;
         uint32_t c[kGroup] = {};
-        if constexpr (SEG) {
-            for (int e = tid; e < a.experts; e += bd) {
-                const uint32_t v = a.totals[e];
+        for (uint32_t i = tid; i < a.pairs; i += bd) {
+            const int e = local_expert(a.ids[i], a.first, a.experts);
 #pragma unroll
-                for (int j = 0; j < kGroup; ++j)
-                    c[j] += e < e0 + j ? v : 0;
-            }
-        } else {
-            for (uint32_t i = tid; i < a.pairs; i += bd) {
-                const int e = local_expert(a.ids[i], a.first, a.experts);
-#pragma unroll
-                for (int j = 0; j < kGroup; ++j)
-                    c[j] += e < e0 + j;
-            }
+            for (int j = 0; j < kGroup; ++j)
+                c[j] += e < e0 + j;
         }
         block_counts<kGroup>(c, lds);
 #pragma unroll
@@ -178,33 +328,12 @@ __global__ __launch_bounds__(256) void k_dispatch(DispatchArgs a)
         for (int j = 0; j < kGroup; ++j)
             key[j] = j < nj ? local_expert(a.ids[i0 + j], a.first, a.experts) : a.experts;
         uint32_t c[kGroup + 1] = {};
-        if constexpr (SEG) {
-            const uint32_t seg = i0 / a.segment;   // the token's pairs lie in one segment
-            for (uint32_t i = seg * a.segment + tid; i < i0 + nj; i += bd) {
-                const int e = local_expert(a.ids[i], a.first, a.experts);
-#pragma unroll
-                for (int j = 0; j < kGroup; ++j)
-                    c[j] += e == key[j] && i < i0 + j;
-            }
-            for (int e = tid; e < a.experts; e += bd) {
-                const uint32_t v = a.totals[e];
-                c[kGroup] += v;
-#pragma unroll
-                for (int j = 0; j < kGroup; ++j)
-                    c[j] += e < key[j] ? v : 0;
-            }
+        for (uint32_t i = tid; i < a.pairs; i += bd) {
+            const int e = local_expert(a.ids[i], a.first, a.experts);
+            c[kGroup] += e < a.experts;
 #pragma unroll
             for (int j = 0; j < kGroup; ++j)
-                if (tid == j && key[j] < a.experts)
-                    c[j] += a.counts[(size_t)key[j] * a.segments + seg];
-        } else {
-            for (uint32_t i = tid; i < a.pairs; i += bd) {
-                const int e = local_expert(a.ids[i], a.first, a.experts);
-                c[kGroup] += e < a.experts;
-#pragma unroll
-                for (int j = 0; j < kGroup; ++j)
-                    c[j] += e < key[j] || (e == key[j] && i < i0 + j);
-            }
+                c[j] += e < key[j] || (e == key[j] && i < i0 + j);
         }
         block_counts<kGroup + 1>(c, lds);
         kept = c[kGroup];
@@ -417,12 +546,20 @@ __global__ __launch_bounds__(256) void k_combine_backward(CombineBwdArgs a)
             st_row<DT, TAIL, true>(static_cast<char*>(a.d_rows) + p * a.ld_d_rows * Elem<DT>::kBytes, v, hidden, zero);
 }
 
-template <int OUT, bool SEG>
+template <int OUT>
 const void* dispatch_fn(int dtype, bool tail)
 {
     if (dtype == 0)
-        return tail ? (const void*)k_dispatch<0, OUT, SEG, true> : (const void*)k_dispatch<0, OUT, SEG, false>;
-    return tail ? (const void*)k_dispatch<1, OUT, SEG, true> : (const void*)k_dispatch<1, OUT, SEG, false>;
+        return tail ? (const void*)k_dispatch<0, OUT, true> : (const void*)k_dispatch<0, OUT, false>;
+    return tail ? (const void*)k_dispatch<1, OUT, true> : (const void*)k_dispatch<1, OUT, false>;
+}
+
+template <int OUT, int NV>
+const void* rows_fn(int dtype, bool tail)
+{
+    if (dtype == 0)
+        return tail ? (const void*)k_dispatch_rows<0, OUT, true, NV> : (const void*)k_dispatch_rows<0, OUT, false, NV>;
+    return tail ? (const void*)k_dispatch_rows<1, OUT, true, NV> : (const void*)k_dispatch_rows<1, OUT, false, NV>;
 }
 
 template <int U>
@@ -443,7 +580,11 @@ const void* backward_fn(int dtype, bool tail)
 
 }  // namespace
 
-uint32_t dispatch_segment(int topk) { return (uint32_t)(kSegment / topk * topk); }
+uint32_t dispatch_segment(size_t pairs)
+{
+    const size_t least = kPlace / 2, per = (pairs + kSegments - 1) / kSegments;
+    return (uint32_t)(per <= least ? least : (per + least - 1) / least * least);
+}
 
 hipError_t launch_dispatch(const DispatchArgs& in, int dtype, int out, hipStream_t s)
 {
@@ -451,12 +592,11 @@ hipError_t launch_dispatch(const DispatchArgs& in, int dtype, int out, hipStream
     void* params[] = {&a};
     const bool seg = a.pairs > kDispatchCountAll;
     if (seg) {
-        hipError_t e = launch_logged("k_dispatch_count", (const void*)k_dispatch_count, dim3(a.segments), dim3(256),
+        hipError_t e = launch_logged("k_dispatch_count", (const void*)k_dispatch_count, dim3(a.segments), dim3(kPlace),
                                      params, s);
         if (e == hipSuccess)
-            e = launch_logged("k_dispatch_scan", (const void*)k_dispatch_scan, dim3((unsigned)a.experts), dim3(256),
-                              params, s);
-        if (e != hipSuccess)
+            e = launch_logged("k_dispatch_place", (const void*)k_dispatch_place, dim3(a.segments), dim3(kPlace), params, s);
+        if (e != hipSuccess || !out)
             return e;
     }
     const size_t nvec = out ? vectors(a.hidden, dtype) : 0;
@@ -473,13 +613,15 @@ hipError_t launch_dispatch(const DispatchArgs& in, int dtype, int out, hipStream
     }
     a.split_vecs = (uint32_t)((nvec + splits - 1) / splits);
     const bool tail = out && partial(a.hidden, dtype);
-    const void* fn;
-    if (seg)
-        fn = out == 0 ? dispatch_fn<0, true>(dtype, tail) : out == 1 ? dispatch_fn<1, true>(dtype, tail)
-                                                                     : dispatch_fn<2, true>(dtype, tail);
-    else
-        fn = out == 0 ? dispatch_fn<0, false>(dtype, tail) : out == 1 ? dispatch_fn<1, false>(dtype, tail)
-                                                                      : dispatch_fn<2, false>(dtype, tail);
+    if (seg) {
+        const size_t nv = (a.split_vecs + wg - 1) / wg;
+        const void* fn = out == 1 ? nv <= 1 ? rows_fn<1, 1>(dtype, tail) : rows_fn<1, 2>(dtype, tail)
+                         : nv <= 1 ? rows_fn<2, 1>(dtype, tail)
+                         : nv <= 2 ? rows_fn<2, 2>(dtype, tail)
+                                   : rows_fn<2, 4>(dtype, tail);
+        return launch_logged("k_dispatch_rows", fn, dim3(a.tokens, (unsigned)splits), dim3(wg), params, s);
+    }
+    const void* fn = out == 0 ? dispatch_fn<0>(dtype, tail) : out == 1 ? dispatch_fn<1>(dtype, tail) : dispatch_fn<2>(dtype, tail);
     const unsigned offset_wgs = (unsigned)(a.experts / kGroup + 1);   // experts + 1 offsets
     return launch_logged("k_dispatch", fn, dim3(a.tokens + offset_wgs, (unsigned)splits), dim3(wg), params, s);
 }

@@ -69,12 +69,11 @@ struct DispatchArgs {
     const void* x;
     void* rows;
     float* row_scales;
-    uint32_t* counts;            // workspace: experts x segments
-    uint32_t* totals;            // workspace: experts
+    uint32_t* counts;            // workspace: segments x experts
     size_t ld_x, ld_rows;        // elements
     size_t hidden;
     uint32_t tokens, pairs;
-    uint32_t segment, segments;  // pairs of a counting segment (whole tokens), their number
+    uint32_t segment, segments;  // pairs of a counting segment, their number
     uint32_t split_vecs;         // vectors of a row one workgroup handles
     int topk, first, experts;
 };
@@ -207,7 +206,7 @@ hipError_t launch_allreduce_lp(const AllreduceLpArgs& a, int nsrc, int dtype, in
 
 
 // The operators around a block's allreduce.
-uint32_t dispatch_segment(int topk);
+uint32_t dispatch_segment(size_t pairs);
 // out: 0 the plan alone, 1 rows copied, 2 rows quantized to INT8
 hipError_t launch_dispatch(const DispatchArgs& a, int dtype, int out, hipStream_t s);
 hipError_t launch_combine(const CombineArgs& a, int dtype, hipStream_t s);

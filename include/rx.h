@@ -469,6 +469,8 @@ size_t rx_residual_norm_backward_workspace(size_t rows, size_t hidden, size_t ga
  *   A = max |x| over the row, s = A / 127, r = 127 / A (each the correctly
  *   rounded FP32 quotient; A == 0, s == 0 or r not finite: s = r = 1),
  *   code = the integer nearest to fl32(x r), ties to even, within -127 .. 127.
+ * A row that holds a NaN gets scale NaN, one that holds an infinity (and no
+ * NaN) an infinite scale, and both codes 0: their products are NaN.
  * x: RX_FP32 or RX_BF16, rows of k elements; codes: ld_codes bytes apart.
  */
 rx_status_t rx_quant_i8(const void* x, size_t ld_x, size_t rows, size_t k,
@@ -486,8 +488,9 @@ rx_status_t rx_quant_i8(const void* x, size_t ld_x, size_t rows, size_t k,
  * and the rows past offsets[experts] become 0.
  *
  * a, b       : INT8; pointers 16-byte aligned; ld_a, ld_b (and stride_b)
- *              multiples of 16, at least k rounded up to 16. The bytes from k
- *              to that multiple are read and may hold anything.
+ *              multiples of 16, at least k rounded up to 16, ld_a and ld_b below
+ *              2^23. The bytes from k to that multiple are read and may hold
+ *              anything.
  * k          : up to 131071 (the exact sum fits 32 bits); k == 0 gives zeros.
  * out        : RX_FP32 or RX_BF16.
  * rows < 2^31, n < 2^31. Offsets outside 0 .. rows are clamped to that range.

@@ -145,6 +145,11 @@ def test_gemm_refusals(want, kw):
     assert gemm(**kw) == want
 
 
+@pytest.mark.parametrize("kw", [dict(lda=1 << 23), dict(ldb=1 << 23), dict(rows=1 << 21, n=1 << 21, ldo=1 << 21)])
+def test_gemm_refuses_what_its_tiles_cannot_address(kw):
+    assert gemm(**kw) == ARG
+
+
 def test_binding_refuses_cpu_tensors(monkeypatch):
     monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
     x = torch.zeros(4, 8)

@@ -141,6 +141,27 @@ def test_dispatch_rows(dtype, strided, tokens, topk, hidden, drop):
     assert torch.equal(rows, R.gather(x, order, topk))
 
 
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("int8", [False, True])
+@pytest.mark.parametrize("tokens,topk,hidden,experts,total", [
+    (4099, 1, 65, 3, 4), (1025, 8, 1000, 100, 256), (70, 60, 2500, 200, 300), (3000, 5, 264, 1024, 1500)])
+def test_dispatch_rows_of_many_pairs(dtype, int8, tokens, topk, hidden, experts, total):
+    g = gen(tokens)
+    ids = routing(g, tokens, topk, total, 0.05)
+    x = randn(g, tokens, hidden, dtype=dtype)
+    _, order, slots, rows, scales = run_dispatch(ids, experts, 2, x, int8=int8, strided=True)
+    want = torch.full((tokens * topk,), -1, dtype=torch.int32)
+    kept = order >= 0
+    want[order[kept].long()] = torch.arange(int(kept.sum()), dtype=torch.int32)
+    assert torch.equal(slots.reshape(-1), want)
+    codes, s = R.quant_i8(x) if int8 else (x, None)
+    assert torch.equal(rows, R.gather(codes, order, topk))
+    if int8:
+        per_row = torch.ones(tokens * topk)
+        per_row[kept] = s[order[kept].long() // topk]
+        assert torch.equal(scales, per_row)
+
+
 def special_rows(x):
     """Rows where quantizing can go wrong: all zero, one value, subnormal, near the largest, ties."""
     h = x.shape[1]
@@ -360,6 +381,24 @@ def test_quant_i8(dtype, rows, k):
     codes.check()
 
 
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("k", [5, 520, 40000])
+def test_quant_i8_rows_that_are_not_finite(dtype, k):
+    x = torch.randn(4, k, generator=gen(k))
+    x[0, 1], x[1, k - 1] = float("nan"), float("inf")
+    x[2, 0], x[2, 2] = float("-inf"), float("nan")
+    x = x.to(dtype)
+    codes, scales = torch.full((4, k), 77, dtype=torch.int8, device="cuda"), torch.empty(4, device="cuda")
+    rx.rx_quant_i8(x.cuda(), codes, scales)
+    want, s = R.quant_i8(x[3:])
+    assert bool((codes[:3] == 0).all()) and torch.equal(codes[3:].cpu(), want) and torch.equal(scales[3:].cpu(), s)
+    assert bool(scales[[0, 2]].isnan().all()) and float(scales[1]) == float("inf")
+    _, order, _, rows, sc = run_dispatch(torch.tensor([[2], [0], [1], [3]], dtype=torch.int32), 4, 0, x, int8=True)
+    at = order.argsort()   # the row of each token
+    assert torch.equal(rows[at], codes.cpu()) and torch.equal(sc[at][[1, 3]], scales[[1, 3]].cpu())
+    assert bool(sc[at][[0, 2]].isnan().all())
+
+
 def padded(t, junk):
     """INT8 rows padded to 16 bytes with values that must not count."""
     k = t.shape[-1]
@@ -408,6 +447,45 @@ def test_gemm_grouped(dtype, counts, pad, n, k):
         lo, hi = int(offsets[e]), int(offsets[e + 1])
         want[lo:hi], bound[lo:hi] = R.gemm_i8(a[lo:hi], sa[lo:hi], b[e], sb[e], dtype)
     within(out.t, want, bound)
+    out.check()
+
+
+TILES = [  # rows and columns that take each kind of tile, with partial ones
+    (4090, 4090), (2041, 4090), (500, 8150), (250, 4100), (30, 4100)]
+
+
+@pytest.mark.parametrize("m,n", TILES)
+@pytest.mark.parametrize("k", [1, 16, 63, 65, 128, 129, 255, 300, 512, 1001])
+def test_gemm_tiles(m, n, k):
+    g = torch.Generator(device="cuda").manual_seed(m + k)
+    rnd = lambda *s: torch.randint(-127, 128, s, generator=g, device="cuda", dtype=torch.int8)
+    a, b = padded(rnd(m, k), 99), padded(rnd(n, k), -77)
+    a[-1], b[-1] = -127, -128
+    sa, sb = torch.ones(m, device="cuda"), torch.ones(n, device="cuda")
+    out = Strided(m, n, FP32)
+    rx.rx_gemm_i8(a, sa, b, sb, out.t)
+    # sums below 2^24 are exact in float32
+    assert torch.equal(out.t.double(), a.double() @ b.double().t())
+    out.check()
+
+
+@pytest.mark.parametrize("counts,pad,n,k", [
+    ([700, 30, 0, 1500, 256, 1, 900], 9, 8001, 200), ([65, 1, 129, 250, 60, 0, 77, 128, 31, 200, 64, 65], 200, 4001, 333),
+    ([128] * 9 + [1, 2, 3], 0, 1000, 260), ([9] * 30, 50, 700, 1025)])
+def test_gemm_grouped_tiles(counts, pad, n, k):
+    rows, experts = sum(counts) + pad, len(counts)
+    g = torch.Generator(device="cuda").manual_seed(rows)
+    rnd = lambda *s: torch.randint(-127, 128, s, generator=g, device="cuda", dtype=torch.int8)
+    a, b = padded(rnd(rows, k), 99), padded(rnd(experts, n, k), -77)
+    sa, sb = torch.ones(rows, device="cuda"), torch.ones(experts, n, device="cuda")
+    offsets = torch.tensor([0] + counts).cumsum(0).to(torch.int32)
+    out = Strided(rows, n, FP32)
+    rx.rx_gemm_i8(a, sa, b, sb, out.t, offsets=gpu(offsets))
+    want = torch.zeros(rows, n, dtype=torch.float64, device="cuda")
+    for e in range(experts):
+        lo, hi = int(offsets[e]), int(offsets[e + 1])
+        want[lo:hi] = a[lo:hi].double() @ b[e].double().t()
+    assert torch.equal(out.t.double(), want)
     out.check()
 
 

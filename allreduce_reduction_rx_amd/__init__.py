@@ -150,9 +150,11 @@ def _ptr_array(values: Sequence[int]):
 
 
 def _stream(stream) -> int:
-    import torch
     if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+        import torch
+        # the current stream's handle without building a Stream object around
+        # it: 0.06 us instead of 2.7, of a call's 6 to 9
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -382,14 +384,8 @@ def rx_allreduce_local_noalloc(bufs: Sequence, algo: int = RX_ALGO_AUTO, fmt="e4
 def _check_block(index: int, dtype, shape, name: str, t) -> int:
     """A GPU tensor of the given shape whose rows are packed (any row stride);
     returns its row stride in elements."""
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a GPU tensor")
-    if t.get_device() != index:
-        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{index}")
-    if t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
-    if t.shape != shape:
-        raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
+    if t.get_device() != index or t.dtype != dtype or t.shape != shape:
+        _refuse_block(index, dtype, shape, name, t)
     if len(shape) < 2:
         if shape and shape[0] > 1 and t.stride(0) != 1:
             raise ValueError(f"{name} must be contiguous")
@@ -399,13 +395,26 @@ def _check_block(index: int, dtype, shape, name: str, t) -> int:
     if width > 1 and stride[-1] != 1:
         raise ValueError(f"{name}'s rows must be contiguous")
     ld = stride[-2]
-    if rows > 1 and ld < width:
-        raise ValueError(f"{name}'s rows overlap")
-    return ld if rows > 1 else max(ld, width)
+    if rows > 1:
+        if ld < width:
+            raise ValueError(f"{name}'s rows overlap")
+        return ld
+    return ld if ld > width else width
+
+
+def _refuse_block(index: int, dtype, shape, name: str, t) -> None:
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a GPU tensor")
+    if t.get_device() != index:
+        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{index}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
+    raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
 
 
 def _check_packed(index: int, dtype, shape, name: str, t) -> None:
-    _check_block(index, dtype, shape, name, t)
+    if t.get_device() != index or t.dtype != dtype or t.shape != shape:
+        _refuse_block(index, dtype, shape, name, t)
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
 

@@ -43,7 +43,7 @@ size_t rx_moe_dispatch_workspace(size_t tokens, int topk, int experts)
     if (!dispatch_sizes_ok(tokens, topk, experts) || tokens * (size_t)topk <= kDispatchCountAll)
         return 0;
     const size_t pairs = tokens * (size_t)topk, seg = dispatch_segment(pairs);
-    return (size_t)experts * ((pairs + seg - 1) / seg) * sizeof(uint32_t);
+    return (size_t)experts * ((pairs + seg - 1) / seg + 1) * sizeof(uint32_t);   // a row to spare
 }
 
 rx_status_t rx_moe_dispatch(const int* expert_ids, size_t tokens, int topk, int first_expert, int experts,
@@ -352,7 +352,7 @@ rx_status_t rx_gemm_i8(const void* a, size_t ld_a, const float* a_scales, const 
         !aligned4(b_scales) || !aligned4(offsets) || !element_aligned(out, out_dtype))
         return RX_ERR_ALIGN;
     // 256 x 256 outputs of 512 threads, a partial tile for every expert: a launch's limit of 2^32 threads
-    if ((rows / 256 + (size_t)experts + 1) * ((n + 255) / 256) >= ((size_t)1 << 23) - 8)
+    if ((rows / 256 + (size_t)experts + 1) * ((n + 255) / 256) >= ((size_t)1 << 23) - 16)
         return RX_ERR_ARG;
     if (rows == 0 || n == 0)
         return RX_OK;

@@ -3,6 +3,8 @@
 // 16-byte vectors, and sums across a wave or a workgroup.
 #pragma once
 
+#include <type_traits>
+
 #include "rx_device.hpp"
 #include "rx_internal.hpp"
 
@@ -147,6 +149,22 @@ __device__ __forceinline__ uint32_t wave_sum_u(uint32_t v)
     v = p[0] + p[1];
     auto q = __builtin_amdgcn_permlane32_swap(v, v, false, false);
     return q[0] + q[1];
+}
+
+// Inclusive sum over the lanes up to this one.
+__device__ __forceinline__ uint32_t wave_incl(uint32_t v)
+{
+    auto from = [](uint32_t x, auto ctrl, auto rows) {
+        return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, ctrl(), rows(), 0xF, false);
+    };
+    using std::integral_constant;
+    v += from(v, integral_constant<int, 0x111>(), integral_constant<int, 0xF>());   // one lane up within 16
+    v += from(v, integral_constant<int, 0x112>(), integral_constant<int, 0xF>());
+    v += from(v, integral_constant<int, 0x114>(), integral_constant<int, 0xF>());
+    v += from(v, integral_constant<int, 0x118>(), integral_constant<int, 0xF>());
+    v += from(v, integral_constant<int, 0x142>(), integral_constant<int, 0xA>());   // lane 15 of a row to the next row
+    v += from(v, integral_constant<int, 0x143>(), integral_constant<int, 0xC>());   // lane 31 to the upper half
+    return v;
 }
 
 // The largest magnitude of a vector, as bits.

@@ -69,40 +69,43 @@ __device__ __forceinline__ void expert_rows(const GemmI8Args& a, int e, uint32_t
     hi = hi > lo ? hi : lo;
 }
 
-__device__ __forceinline__ uint32_t wave_incl(uint32_t v, int lane)
-{
-#pragma unroll
-    for (int d = 1; d < kWave; d *= 2) {
-        const uint32_t o = __shfl_up(v, d);
-        if (lane >= d)
-            v += o;
-    }
-    return v;
-}
-
 // The row tiles of a call: each expert's rows start a tile of their own;
-// past the last, tiles of the rows that no expert owns.
+// past the last, tiles of the rows that no expert owns. Every wave counts
+// them for itself, 64 experts at a time, and keeps the first 64.
 struct Tiles {
     uint32_t owned, end, total;   // tiles with an expert; the last expert's end; all tiles
+    uint32_t lo, hi, incl;        // expert `lane`: its rows, the tiles up to its last
 };
+
+__device__ __forceinline__ uint32_t tiles_to(const GemmI8Args& a, int e, uint32_t bm, uint32_t& lo, uint32_t& hi)
+{
+    lo = hi = 0;
+    if (e < a.experts)
+        expert_rows(a, e, lo, hi);
+    return wave_incl((hi - lo + bm - 1) / bm);
+}
 
 __device__ __forceinline__ Tiles count_tiles(const GemmI8Args& a, uint32_t bm)
 {
+    Tiles t = {};
     if (!a.offsets) {
-        const uint32_t t = (a.rows + bm - 1) / bm;
-        return {t, a.rows, t};
+        t.owned = t.total = (a.rows + bm - 1) / bm;
+        t.end = a.rows;
+        return t;
     }
-    uint32_t n = 0, end = 0;
     for (int e0 = 0; e0 < a.experts; e0 += kWave) {
-        const int e = e0 + lane_id();
-        uint32_t lo = 0, hi = 0;
-        if (e < a.experts)
-            expert_rows(a, e, lo, hi);
-        n += (hi - lo + bm - 1) / bm;
-        end = (uint32_t)__builtin_amdgcn_readlane((int)hi, (a.experts - e0 < kWave ? a.experts - e0 : kWave) - 1);
+        uint32_t lo, hi;
+        const uint32_t incl = tiles_to(a, e0 + lane_id(), bm, lo, hi);
+        if (e0 == 0) {
+            t.lo = lo;
+            t.hi = hi;
+            t.incl = incl;
+        }
+        t.owned += (uint32_t)__builtin_amdgcn_readlane((int)incl, kWave - 1);
+        t.end = (uint32_t)__builtin_amdgcn_readlane((int)hi, (a.experts - e0 < kWave ? a.experts - e0 : kWave) - 1);
     }
-    const uint32_t owned = (uint32_t)__builtin_amdgcn_readfirstlane((int)wave_sum_u(n));
-    return {owned, end, owned + (a.rows - end + bm - 1) / bm};
+    t.total = t.owned + (a.rows - t.end + bm - 1) / bm;
+    return t;
 }
 
 // The rows [lo, hi) of row tile `tm` and their expert, -1 past the last's.
@@ -121,24 +124,21 @@ __device__ __forceinline__ TileRows find_tile(const GemmI8Args& a, const Tiles& 
         const uint32_t lo = t.end + (tm - t.owned) * bm;
         return {lo, lo + bm < a.rows ? lo + bm : a.rows, -1};
     }
-    const int lane = lane_id();
-    uint32_t base = 0;
-    for (int e0 = 0;; e0 += kWave) {
-        const int e = e0 + lane;
-        uint32_t lo = 0, hi = 0;
-        if (e < a.experts)
-            expert_rows(a, e, lo, hi);
-        const uint32_t tiles = (hi - lo + bm - 1) / bm;
-        const uint32_t incl = wave_incl(tiles, lane);
+    uint32_t base = 0, lo = t.lo, hi = t.hi, incl = t.incl;
+    for (int e0 = 0;;) {
         const uint64_t past = __ballot(base + incl > tm);
         if (past) {
             const int l = __builtin_ctzll(past);
-            const uint32_t first = base + (uint32_t)__builtin_amdgcn_readlane((int)(incl - tiles), l);
-            const uint32_t rlo = (uint32_t)__builtin_amdgcn_readlane((int)lo, l) + (tm - first) * bm;
+            const uint32_t own = (uint32_t)__builtin_amdgcn_readlane((int)incl, l) + base;   // tiles up to its last
+            const uint32_t rlo = (uint32_t)__builtin_amdgcn_readlane((int)lo, l);
             const uint32_t rhi = (uint32_t)__builtin_amdgcn_readlane((int)hi, l);
-            return {rlo, rlo + bm < rhi ? rlo + bm : rhi, e0 + l};
+            const uint32_t first = own - (rhi - rlo + bm - 1) / bm;
+            const uint32_t at = rlo + (tm - first) * bm;
+            return {at, at + bm < rhi ? at + bm : rhi, e0 + l};
         }
         base += (uint32_t)__builtin_amdgcn_readlane((int)incl, kWave - 1);
+        e0 += kWave;
+        incl = tiles_to(a, e0 + lane_id(), bm, lo, hi);
     }
 }
 
@@ -146,15 +146,23 @@ constexpr uint32_t kTileGroup = 8;
 
 // Workgroup -> tile. Workgroups go to the XCDs in turn, and each XCD has its
 // own L2: an XCD takes a run of tiles of its own, eight row tiles by the
-// columns, so that the 32 it works on together share rows and columns.
-__device__ __forceinline__ bool pick_tile(uint32_t ntm, uint32_t ntn, uint32_t& tm, uint32_t& tn)
+// columns, so that the 32 it works on together share rows and columns. The
+// tiles without an expert come after, dealt to all XCDs alike.
+__device__ __forceinline__ bool pick_tile(const Tiles& t, uint32_t ntn, uint32_t& tm, uint32_t& tn)
 {
-    const uint32_t total = ntm * ntn, per = (total + kXcds - 1) / kXcds;
-    const uint32_t i = blockIdx.x / kXcds, tile = (blockIdx.x % kXcds) * per + i;
-    if (i >= per || tile >= total)
+    const uint32_t owned = t.owned * ntn, per = (owned + kXcds - 1) / kXcds;
+    const uint32_t i = blockIdx.x / kXcds, xcd = blockIdx.x % kXcds;
+    if (i >= per) {
+        const uint32_t tile = (i - per) * kXcds + xcd;
+        tm = t.owned + tile / ntn;
+        tn = tile % ntn;
+        return tm < t.total;
+    }
+    const uint32_t tile = xcd * per + i;
+    if (tile >= owned)
         return false;
     const uint32_t group = tile / (kTileGroup * ntn), in = tile % (kTileGroup * ntn), first = group * kTileGroup;
-    const uint32_t size = ntm - first < kTileGroup ? ntm - first : kTileGroup;
+    const uint32_t size = t.owned - first < kTileGroup ? t.owned - first : kTileGroup;
     tm = first + in % size;
     tn = in / size;
     return true;
@@ -299,7 +307,7 @@ __global__ __launch_bounds__(WM * WN * kWave, 1) void k_gemm_i8(GemmI8Args a)
     const int tid = threadIdx.x, lane = lane_id(), wave = __builtin_amdgcn_readfirstlane(tid / kWave);
     const Tiles tiles = count_tiles(a, BM);
     uint32_t tm, tn;
-    if (!pick_tile(tiles.total, (a.n + BN - 1) / BN, tm, tn))
+    if (!pick_tile(tiles, (a.n + BN - 1) / BN, tm, tn))
         return;
     const uint32_t n0 = tn * BN;
     const TileRows rows = find_tile(a, tiles, tm, BM);
@@ -467,7 +475,7 @@ __global__ __launch_bounds__(W * kWave) void k_gemm_i8_split(GemmI8Args a)
     const int tid = threadIdx.x, lane = lane_id(), wave = __builtin_amdgcn_readfirstlane(tid / kWave);
     const Tiles tiles = count_tiles(a, BM);
     uint32_t tm, tn;
-    if (!pick_tile(tiles.total, (a.n + BN - 1) / BN, tm, tn))
+    if (!pick_tile(tiles, (a.n + BN - 1) / BN, tm, tn))
         return;
     const uint32_t n0 = tn * BN;
     const TileRows rows = find_tile(a, tiles, tm, BM);
@@ -619,7 +627,8 @@ size_t row_tiles(const GemmI8Args& a, size_t bm)
 hipError_t launch_grid(GemmI8Args& a, const void* fn, const char* name, size_t bm, size_t bn, unsigned threads, hipStream_t s)
 {
     void* params[] = {&a};
-    const size_t grid = (row_tiles(a, bm) * ((a.n + bn - 1) / bn) + kXcds - 1) / kXcds * kXcds;
+    // whole rounds of the XCDs for the tiles with an expert and for those without
+    const size_t grid = (row_tiles(a, bm) * ((a.n + bn - 1) / bn) + 2 * kXcds) / kXcds * kXcds;
     return launch_logged(name, fn, dim3((unsigned)grid), dim3(threads), params, s);
 }
 
@@ -656,7 +665,7 @@ double estimate(const GemmI8Args& a, double bm, double bn, double slots, double 
         tm = tm < owners ? owners : tm;
     }
     const double tn = (double)((a.n + (size_t)bn - 1) / (size_t)bn), t = tm * tn / slots;
-    if (((double)row_tiles(a, (size_t)bm) * tn + 8.0) * 512.0 >= 4294967296.0)
+    if (((double)row_tiles(a, (size_t)bm) * tn + 16.0) * 512.0 >= 4294967296.0)
         return 1e300;   // threads of one launch
     return us * (t <= 1.0 ? 1.0 : a.offsets ? t + 0.25 : (double)(size_t)(t + 0.9999));
 }

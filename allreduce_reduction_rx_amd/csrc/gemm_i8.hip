@@ -1,6 +1,8 @@
 // gemm_i8.hip -- rows to 8-bit integers with a scale each, and the product of
 // such matrices with a scale per token and channel, dense or grouped by
 // expert (gfx950). Defined in rx.h.
+#include <math.h>
+
 #include <utility>
 
 #include "block_common.hpp"
@@ -646,17 +648,23 @@ hipError_t launch_split(GemmI8Args& a, int out_dtype, hipStream_t s)
     return launch_grid(a, fn, "k_gemm_i8_split", 16 * MT, 16 * NT, W * kWave, s);
 }
 
-// The tile with the least estimated time. A tile costs what a round of its
-// kind takes for 128 bytes of k with the GPU full, measured: 1.71 us for 256 x
-// 256 (8192^3, 439 us in four rounds), 1.05 for 128 x 256 (2048 x 4096 x 4096,
-// 34 us), 0.65 for 128 x 128 (512 x 8192 x 8192, 42 us), 0.53 for two 64 x 64
-// a CU (the same, 68 us), 0.36 for two 32 x 32 of split k (64 x 8192 x 8192, 23
-// us). A call fills whole rounds; with experts the number of tiles is known
-// to the half of each expert's last, so a started round counts a quarter.
-// Where each would go wrong: 32 x 8192 x 8192 takes 16 us split and 81 us in 256 x 256
-// tiles; 32768 x 4096 x 4096 over 32 experts 589 us in 256 x 256, 750 us in 128 x 128
-// and 1080 us in 64 x 64.
-double estimate(const GemmI8Args& a, double bm, double bn, double slots, double us)
+// Estimated time, in microseconds for every 128 bytes of k. `us` is what a
+// round of a kind takes with the GPU full, measured: 1.71 for 256 x 256 (8192^3,
+// 439 us in four rounds), 1.05 for 128 x 256 (2048 x 4096 x 4096, 34 us), 0.65
+// for 128 x 128 with eight waves (512 x 8192 x 8192, 42 us), 1.14 for two of 128 x
+// 128 with four waves a CU (8192^3, 586 us), 0.53 for two of 64 x 64 (512 x 8192
+// x 8192, 68 us), 0.36 for two of 32 x 32 with split k (64 x 8192 x 8192, 23 us).
+//
+// A call pays whole rounds where a CU has one workgroup at a time (one tile
+// more than 256 cost 44 us instead of 27 us in a call over 24 experts); with
+// two, the last round's run faster alone. With experts the number of tiles
+// is known to about half a tile each, half a round in the mean.
+//
+// Where each would go wrong: 32 x 8192 x 8192 takes 14 us split and 57 us in
+// 256 x 256; 32116 rows of 32 experts x 4096 x 4096 take 571 us in 256 x 256, 602 in
+// 128 x 256, 732 in 128 x 128, 1048 in 64 x 64 and 1851 split; 2007 rows of 24
+// experts x 2100 x 2056 take 32 us in two of 128 x 128, 44 in 128 x 256, 37 in 256 x 256.
+double estimate(const GemmI8Args& a, double bm, double bn, double per_cu, double us)
 {
     double tm = (double)((a.rows + (size_t)bm - 1) / (size_t)bm);
     if (a.offsets) {
@@ -664,27 +672,32 @@ double estimate(const GemmI8Args& a, double bm, double bn, double slots, double 
         tm = a.rows / bm + 0.5 * owners;
         tm = tm < owners ? owners : tm;
     }
-    const double tn = (double)((a.n + (size_t)bn - 1) / (size_t)bn), t = tm * tn / slots;
+    const double tn = (double)((a.n + (size_t)bn - 1) / (size_t)bn), t = tm * tn / (per_cu * device_cu_count());
     if (((double)row_tiles(a, (size_t)bm) * tn + 16.0) * 512.0 >= 4294967296.0)
         return 1e300;   // threads of one launch
-    return us * (t <= 1.0 ? 1.0 : a.offsets ? t + 0.25 : (double)(size_t)(t + 0.9999));
+    const double whole = ceil(t);
+    if (t <= 1.0)
+        return us;
+    if (per_cu > 1.0)
+        return us * (t + 0.25 < whole ? t + 0.25 : whole);
+    return us * (a.offsets ? t + 0.5 : whole);
 }
 
 hipError_t launch_gemm_i8(const GemmI8Args& in, int out_dtype, hipStream_t s)
 {
     GemmI8Args a = in;
-    const double cus = device_cu_count();
-    const double cost[] = {estimate(a, 256, 256, cus, 1.71), estimate(a, 128, 256, cus, 1.05), estimate(a, 128, 128, cus, 0.65),
-                           estimate(a, 64, 64, 2 * cus, 0.53), estimate(a, 32, 32, 2 * cus, 0.36)};
+    const double cost[] = {estimate(a, 256, 256, 1, 1.71), estimate(a, 128, 256, 1, 1.05), estimate(a, 128, 128, 1, 0.65),
+                           estimate(a, 128, 128, 2, 1.14), estimate(a, 64, 64, 2, 0.53), estimate(a, 32, 32, 2, 0.36)};
     int best = 0;
-    for (int i = 1; i < 5; ++i)
+    for (int i = 1; i < 6; ++i)
         if (cost[i] < cost[best])
             best = i;
     switch (best) {
     case 0: return launch_tiles<256, 256, 4, 2, 2>(a, out_dtype, s);
     case 1: return launch_tiles<128, 256, 2, 4, 3>(a, out_dtype, s);
     case 2: return launch_tiles<128, 128, 2, 4, 4>(a, out_dtype, s);
-    case 3: return launch_tiles<64, 64, 2, 2, 4>(a, out_dtype, s);
+    case 3: return launch_tiles<128, 128, 2, 2, 2>(a, out_dtype, s);
+    case 4: return launch_tiles<64, 64, 2, 2, 4>(a, out_dtype, s);
     default: return launch_split<2, 2, 4, 2>(a, out_dtype, s);
     }
 }

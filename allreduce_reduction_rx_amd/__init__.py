@@ -1,4 +1,6 @@
 """Python binding of librx (``include/rx.h``): argument marshalling only.
+(The operators around a block's allreduce are marshalled by ``_rxbind.so``,
+csrc/bind.cpp: their calls are short enough for it to count.)
 
 Every function here has the name of the C entry point it calls and takes
 torch tensors that live on the GPU; it checks dtype, device, contiguity and
@@ -381,54 +383,34 @@ def rx_allreduce_local_noalloc(bufs: Sequence, algo: int = RX_ALGO_AUTO, fmt="e4
 
 # ---- the operators around a block's allreduce ---------------------------------
 
-def _check_block(index: int, dtype, shape, name: str, t) -> int:
-    """A GPU tensor of the given shape whose rows are packed (any row stride);
-    returns its row stride in elements."""
-    if t.get_device() != index or t.dtype != dtype or t.shape != shape:
-        _refuse_block(index, dtype, shape, name, t)
-    if len(shape) < 2:
-        if shape and shape[0] > 1 and t.stride(0) != 1:
-            raise ValueError(f"{name} must be contiguous")
-        return 0
-    rows, width = shape[-2], shape[-1]
-    stride = t.stride()
-    if width > 1 and stride[-1] != 1:
-        raise ValueError(f"{name}'s rows must be contiguous")
-    ld = stride[-2]
-    if rows > 1:
-        if ld < width:
-            raise ValueError(f"{name}'s rows overlap")
-        return ld
-    return ld if ld > width else width
+_bound = None
 
 
-def _refuse_block(index: int, dtype, shape, name: str, t) -> None:
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a GPU tensor")
-    if t.get_device() != index:
-        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{index}")
-    if t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
-    raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
+def _bind():
+    """The compiled marshalling module, connected to the loaded librx."""
+    global _bound
+    if _bound is None:
+        import importlib.util
+
+        import torch
+        L = lib()
+        path = os.path.join(_HERE, "_rxbind.so")
+        if not os.path.exists(path):
+            raise RuntimeError(f"{path} is missing: build it with __graft_entry__.build()")
+        spec = importlib.util.spec_from_file_location("_rxbind", path)
+        m = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(m)
+        m.connect(torch._C._cuda_getCurrentRawStream, *(ctypes.cast(fn, ctypes.c_void_p).value for fn in (
+            L.rx_moe_dispatch, L.rx_moe_combine, L.rx_moe_combine_backward, L.rx_residual_norm,
+            L.rx_residual_norm_backward, L.rx_quant_i8, L.rx_gemm_i8)))
+        _bound = m
+    return _bound
 
 
-def _check_packed(index: int, dtype, shape, name: str, t) -> None:
-    if t.get_device() != index or t.dtype != dtype or t.shape != shape:
-        _refuse_block(index, dtype, shape, name, t)
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-
-
-def _opt(t):
-    return None if t is None else t.data_ptr()
-
-
-def _workspace(workspace, index: int):
+def _here(stream):
+    """The current device, and the stream's handle (None: the current one)."""
     import torch
-    if workspace is None:
-        return None, 0
-    _check_packed(index, torch.uint8, workspace.shape, "workspace", workspace)
-    return workspace.data_ptr(), workspace.numel()
+    return torch.cuda.current_device(), None if stream is None else _stream(stream)
 
 
 def rx_moe_dispatch_workspace(tokens: int, topk: int, experts: int) -> int:
@@ -442,109 +424,23 @@ def rx_moe_dispatch(expert_ids, experts: int, offsets, order, slots, x=None, row
     (int32, experts + 1), order (int32, tokens topk) and slots (int32, tokens x
     topk); with x (tokens x hidden), rows (tokens topk x hidden, x's dtype, or
     int8 with scales, float32) receives the tokens in that order."""
-    import torch
-    dev, i32 = torch.cuda.current_device(), torch.int32
-    tokens, topk = expert_ids.shape
-    pairs = tokens * topk
-    _check_packed(dev, i32, (tokens, topk), "expert_ids", expert_ids)
-    _check_packed(dev, i32, (experts + 1,), "offsets", offsets)
-    _check_packed(dev, i32, (pairs,), "order", order)
-    _check_packed(dev, i32, (tokens, topk), "slots", slots)
-    hidden = ld_x = ld_rows = 0
-    xdt = rdt = RX_FP32
-    if x is not None or rows is not None or scales is not None:
-        if x is None or rows is None:
-            raise ValueError("x and rows come together")
-        hidden, xdt = x.shape[-1], _rx_dtype(x)
-        ld_x = _check_block(dev, x.dtype, (tokens, hidden), "x", x)
-        quant = rows.dtype == torch.int8
-        if quant != (scales is not None):
-            raise ValueError("scales come with int8 rows")
-        rdt = RX_INT8 if quant else xdt
-        ld_rows = _check_block(dev, torch.int8 if quant else x.dtype, (pairs, hidden), "rows", rows)
-        if quant:
-            _check_packed(dev, torch.float32, (pairs,), "scales", scales)
-    ws, nbytes = _workspace(workspace, dev)
-    _check(lib().rx_moe_dispatch(expert_ids.data_ptr(), tokens, topk, first_expert, experts, _opt(x),
-                                 ld_x, hidden, xdt, offsets.data_ptr(), order.data_ptr(),
-                                 slots.data_ptr(), _opt(rows), ld_rows, rdt, _opt(scales), ws, nbytes,
-                                 _stream(stream)), "rx_moe_dispatch")
+    _check((_bound or _bind()).moe_dispatch(*_here(stream), expert_ids, experts, offsets, order, slots, x,
+                                            rows, scales, first_expert, workspace), "rx_moe_dispatch")
 
 
 def rx_moe_combine(rows, slots, weights, out, stream=None) -> None:
     """out[t] = sum over j of weights[t, j] rows[slots[t, j]] (dropped pairs left
     out); weights float32, or None for ones: the gradient of rx_moe_dispatch's
     gather."""
-    import torch
-    dev = torch.cuda.current_device()
-    tokens, topk = slots.shape
-    nrows, hidden = rows.shape
-    dt = _rx_dtype(rows)
-    ld_rows = _check_block(dev, rows.dtype, (nrows, hidden), "rows", rows)
-    ld_out = _check_block(dev, rows.dtype, (tokens, hidden), "out", out)
-    _check_packed(dev, torch.int32, (tokens, topk), "slots", slots)
-    if weights is not None:
-        _check_packed(dev, torch.float32, (tokens, topk), "weights", weights)
-    _check(lib().rx_moe_combine(rows.data_ptr(), ld_rows, nrows, slots.data_ptr(), _opt(weights),
-                                tokens, topk, hidden, dt, out.data_ptr(), ld_out, _stream(stream)),
-           "rx_moe_combine")
+    _check((_bound or _bind()).moe_combine(*_here(stream), rows, slots, weights, out), "rx_moe_combine")
 
 
 def rx_moe_combine_backward(d_out, rows, slots, weights, offsets, d_rows, d_weights=None,
                             stream=None) -> None:
     """Gradient of rx_moe_combine for a plan of rx_moe_dispatch: d_rows (rows that
     no pair owns are 0) and, when given, d_weights (then rows are needed)."""
-    import torch
-    dev = torch.cuda.current_device()
-    tokens, topk = slots.shape
-    nrows, hidden = d_rows.shape
-    dt = _rx_dtype(d_out)
-    ld_g = _check_block(dev, d_out.dtype, (tokens, hidden), "d_out", d_out)
-    ld_dr = _check_block(dev, d_out.dtype, (nrows, hidden), "d_rows", d_rows)
-    ld_r = 0
-    if rows is not None:
-        ld_r = _check_block(dev, d_out.dtype, (nrows, hidden), "rows", rows)
-    elif d_weights is not None:
-        raise ValueError("d_weights needs rows")
-    _check_packed(dev, torch.int32, (tokens, topk), "slots", slots)
-    _check_packed(dev, torch.int32, offsets.shape, "offsets", offsets)
-    if offsets.numel() < 1:
-        raise ValueError("offsets must hold experts + 1 values")
-    for name, t in (("weights", weights), ("d_weights", d_weights)):
-        if t is not None:
-            _check_packed(dev, torch.float32, (tokens, topk), name, t)
-    _check(lib().rx_moe_combine_backward(
-        d_out.data_ptr(), ld_g, _opt(rows), ld_r, nrows, slots.data_ptr(), _opt(weights),
-        offsets.data_ptr() + 4 * (offsets.numel() - 1), tokens, topk, hidden, dt, d_rows.data_ptr(),
-        ld_dr, _opt(d_weights), _stream(stream)), "rx_moe_combine_backward")
-
-
-def _norm_inputs(srcs, residual, gate, gate_rows, w_post, w_pre):
-    """Checks what both directions of rx_residual_norm read; returns (device,
-    rows, hidden, dtype, gate_rows, source stride, residual stride)."""
-    import torch
-    dev = torch.cuda.current_device()
-    rows, hidden = srcs[0].shape
-    dtype = srcs[0].dtype
-    _rx_dtype(srcs[0])
-    ld_src = _check_block(dev, dtype, (rows, hidden), "srcs[0]", srcs[0])
-    for k in range(1, len(srcs)):
-        if _check_block(dev, dtype, (rows, hidden), "a source", srcs[k]) != ld_src:
-            raise ValueError(f"srcs[{k}] has another row stride than srcs[0]")
-    ld_res = 0
-    if residual is not None:
-        ld_res = _check_block(dev, dtype, (rows, hidden), "residual", residual)
-    if gate_rows is None:
-        gate_rows = max(1, rows)
-    if gate is not None:
-        if gate_rows < 1:
-            raise ValueError("gate_rows must be positive")
-        _check_packed(dev, dtype, (-(-rows // gate_rows), hidden), "gate", gate)
-    if w_post is not None:
-        _check_packed(dev, dtype, (hidden,), "w_post", w_post)
-    if w_pre is not None:
-        _check_packed(dev, dtype, (hidden,), "w_pre", w_pre)
-    return dev, rows, hidden, dtype, gate_rows, ld_src, ld_res
+    _check((_bound or _bind()).moe_combine_backward(*_here(stream), d_out, rows, slots, weights, offsets,
+                                                    d_rows, d_weights), "rx_moe_combine_backward")
 
 
 def rx_residual_norm(srcs: Sequence, residual, gate, w_post, w_pre, out_h, out_z, rstd_post=None,
@@ -553,20 +449,9 @@ def rx_residual_norm(srcs: Sequence, residual, gate, w_post, w_pre, out_h, out_z
     """h = residual_scale residual + gate norm(sum of srcs) w_post, z = norm(h)
     w_pre, RMS norms in FP32. residual, gate, w_post and one of out_h, out_z
     may be None. gate has a row for every gate_rows rows (None: one row)."""
-    import torch
-    dev, rows, hidden, dtype, gate_rows, ld_src, ld_res = _norm_inputs(srcs, residual, gate,
-                                                                       gate_rows, w_post, w_pre)
-    ld_h = _check_block(dev, dtype, (rows, hidden), "out_h", out_h) if out_h is not None else 0
-    ld_z = _check_block(dev, dtype, (rows, hidden), "out_z", out_z) if out_z is not None else 0
-    if rstd_post is not None:
-        _check_packed(dev, torch.float32, (rows,), "rstd_post", rstd_post)
-    if rstd_pre is not None:
-        _check_packed(dev, torch.float32, (rows,), "rstd_pre", rstd_pre)
-    _check(lib().rx_residual_norm(
-        _ptr_array([s.data_ptr() for s in srcs]), len(srcs), ld_src, _opt(residual), ld_res,
-        _opt(gate), gate_rows, _opt(w_post), _opt(w_pre), residual_scale, eps, rows, hidden,
-        RX_BF16 if dtype == torch.bfloat16 else RX_FP32, _opt(out_h), ld_h, _opt(out_z), ld_z,
-        _opt(rstd_post), _opt(rstd_pre), _stream(stream)), "rx_residual_norm")
+    _check((_bound or _bind()).residual_norm(*_here(stream), srcs, residual, gate, gate_rows, w_post, w_pre,
+                                             out_h, out_z, rstd_post, rstd_pre, residual_scale, eps),
+           "rx_residual_norm")
 
 
 def rx_residual_norm_backward_workspace(rows: int, hidden: int, gate_rows: Optional[int] = None) -> int:
@@ -583,50 +468,15 @@ def rx_residual_norm_backward(srcs: Sequence, residual, gate, w_post, w_pre, rst
     forward call's inputs and rstd_post, rstd_pre: d_src (every source's),
     d_residual, and in float32 d_gate, d_w_post, d_w_pre; each of the last four
     may be None."""
-    import torch
-    dev, rows, hidden, dtype, gate_rows, ld_src, ld_res = _norm_inputs(srcs, residual, gate,
-                                                                       gate_rows, w_post, w_pre)
-    f32 = torch.float32
-    lds = []
-    for name, t in (("d_h", d_h), ("d_z", d_z), ("d_src", d_src), ("d_residual", d_residual)):
-        lds.append(0 if t is None else _check_block(dev, dtype, (rows, hidden), name, t))
-    for name, t in (("rstd_post", rstd_post), ("rstd_pre", rstd_pre)):
-        if t is not None:
-            _check_packed(dev, f32, (rows,), name, t)
-    for name, t in (("d_w_post", d_w_post), ("d_w_pre", d_w_pre)):
-        if t is not None:
-            _check_packed(dev, f32, (hidden,), name, t)
-    if d_gate is not None:
-        _check_packed(dev, f32, (-(-rows // gate_rows), hidden), "d_gate", d_gate)
-    ws, nbytes = _workspace(workspace, dev)
-    _check(lib().rx_residual_norm_backward(
-        _ptr_array([s.data_ptr() for s in srcs]), len(srcs), ld_src, _opt(residual), ld_res,
-        _opt(gate), gate_rows, _opt(w_post), _opt(w_pre), _opt(rstd_post), _opt(rstd_pre),
-        residual_scale, rows, hidden, RX_BF16 if dtype == torch.bfloat16 else RX_FP32, _opt(d_h),
-        lds[0], _opt(d_z), lds[1], _opt(d_src), lds[2], _opt(d_residual), lds[3], _opt(d_gate),
-        _opt(d_w_post), _opt(d_w_pre), ws, nbytes, _stream(stream)), "rx_residual_norm_backward")
+    _check((_bound or _bind()).residual_norm_backward(
+        *_here(stream), srcs, residual, gate, gate_rows, w_post, w_pre, rstd_post, rstd_pre, d_h, d_z,
+        d_src, d_residual, d_gate, d_w_post, d_w_pre, residual_scale, workspace),
+        "rx_residual_norm_backward")
 
 
 def rx_quant_i8(x, codes, scales, stream=None) -> None:
     """Rows of x (float32 or bfloat16) to int8 codes and a float32 scale a row."""
-    import torch
-    dev = torch.cuda.current_device()
-    rows, k = x.shape
-    dt = _rx_dtype(x)
-    ld_x = _check_block(dev, x.dtype, (rows, k), "x", x)
-    ld_c = _check_block(dev, torch.int8, (rows, k), "codes", codes)
-    _check_packed(dev, torch.float32, (rows,), "scales", scales)
-    _check(lib().rx_quant_i8(x.data_ptr(), ld_x, rows, k, dt, codes.data_ptr(), ld_c,
-                             scales.data_ptr(), _stream(stream)), "rx_quant_i8")
-
-
-def _check_padded(t, k: int, ld: int, name: str) -> None:
-    """The product reads whole 16-byte chunks: the last row's must lie in the
-    tensor's storage too."""
-    if k % 16 and t.numel():
-        last = t.storage_offset() + sum((n - 1) * s for n, s in zip(t.shape[:-1], t.stride()[:-1]))
-        if last + -(-k // 16) * 16 > t.untyped_storage().nbytes():
-            raise ValueError(f"{name}'s last row must be padded to a multiple of 16 bytes")
+    _check((_bound or _bind()).quant_i8(*_here(stream), x, codes, scales), "rx_quant_i8")
 
 
 def rx_gemm_i8(a, a_scales, b, b_scales, out, offsets=None, stream=None) -> None:
@@ -634,27 +484,7 @@ def rx_gemm_i8(a, a_scales, b, b_scales, out, offsets=None, stream=None) -> None
     a (rows x k) and b (n x k), or with offsets (int32, experts + 1, of
     rx_moe_dispatch) b (experts x n x k), rows offsets[e] .. offsets[e + 1] - 1
     times b[e]. Row strides are multiples of 16 (pad the rows)."""
-    import torch
-    dev, i8, f32 = torch.cuda.current_device(), torch.int8, torch.float32
-    rows, k = a.shape
-    n = b.shape[-2]
-    experts = b.shape[0] if offsets is not None else 1
-    shape = (n, k) if offsets is None else (experts, n, k)
-    ld_a = _check_block(dev, i8, (rows, k), "a", a)
-    ld_b = _check_block(dev, i8, shape, "b", b)
-    stride_b = 0
-    if offsets is not None:
-        _check_packed(dev, torch.int32, (experts + 1,), "offsets", offsets)
-        stride_b = b.stride(0)
-    _check_packed(dev, f32, (rows,), "a_scales", a_scales)
-    _check_packed(dev, f32, shape[:-1], "b_scales", b_scales)
-    dt = _rx_dtype(out)
-    ld_o = _check_block(dev, out.dtype, (rows, n), "out", out)
-    _check_padded(a, k, ld_a, "a")
-    _check_padded(b, k, ld_b, "b")
-    _check(lib().rx_gemm_i8(a.data_ptr(), ld_a, a_scales.data_ptr(), b.data_ptr(), ld_b, stride_b,
-                            b_scales.data_ptr(), _opt(offsets), experts, rows, n, k, out.data_ptr(),
-                            ld_o, dt, _stream(stream)), "rx_gemm_i8")
+    _check((_bound or _bind()).gemm_i8(*_here(stream), a, a_scales, b, b_scales, out, offsets), "rx_gemm_i8")
 
 
 # ---- test hooks (rx_testhooks.h) -------------------------------------------

@@ -9,39 +9,59 @@
 namespace rx {
 namespace {
 
+// y = the sources' sum, B sources' loads of a thread in flight together.
 template <int DT, bool TAIL, int NV>
 __device__ __forceinline__ void fold_row(const void* const* src, int nsrc, size_t row_bytes, int hidden,
                                          float (*y)[Elem<DT>::kVE])
 {
+    constexpr int B = NV == 1 ? 8 : 4;   // more would cost a longer row its occupancy
+    const int tid = (int)threadIdx.x, bd = (int)blockDim.x;
     int r;
-    switch (nsrc) {
-    case 1: fold_batch<DT, TAIL, NV, 1, true>(src, 0, row_bytes, hidden, (int)threadIdx.x, (int)blockDim.x, y); return;
-    case 2: fold_batch<DT, TAIL, NV, 2, true>(src, 0, row_bytes, hidden, (int)threadIdx.x, (int)blockDim.x, y); return;
-    case 3: fold_batch<DT, TAIL, NV, 3, true>(src, 0, row_bytes, hidden, (int)threadIdx.x, (int)blockDim.x, y); return;
-    default: fold_batch<DT, TAIL, NV, 4, true>(src, 0, row_bytes, hidden, (int)threadIdx.x, (int)blockDim.x, y); r = 4;
+    switch (nsrc < B ? nsrc : B) {
+    case 1: fold_batch<DT, TAIL, NV, 1, true>(src, 0, row_bytes, hidden, tid, bd, y); return;
+    case 2: fold_batch<DT, TAIL, NV, 2, true>(src, 0, row_bytes, hidden, tid, bd, y); return;
+    case 3: fold_batch<DT, TAIL, NV, 3, true>(src, 0, row_bytes, hidden, tid, bd, y); return;
+    case 8: fold_batch<DT, TAIL, NV, B, true>(src, 0, row_bytes, hidden, tid, bd, y); r = B; break;
+    default: fold_batch<DT, TAIL, NV, 4, true>(src, 0, row_bytes, hidden, tid, bd, y); r = 4;
     }
     for (; r + 4 <= nsrc; r += 4)
-        fold_batch<DT, TAIL, NV, 4, false>(src, r, row_bytes, hidden, (int)threadIdx.x, (int)blockDim.x, y);
+        fold_batch<DT, TAIL, NV, 4, false>(src, r, row_bytes, hidden, tid, bd, y);
     for (; r < nsrc; ++r)
-        fold_batch<DT, TAIL, NV, 1, false>(src, r, row_bytes, hidden, (int)threadIdx.x, (int)blockDim.x, y);
+        fold_batch<DT, TAIL, NV, 1, false>(src, r, row_bytes, hidden, tid, bd, y);
 }
 
+// NV 1: the gate and the weights are loaded before the sources too, so that a
+// row has one round trip to memory (32 rows of 8192 BF16 over 8 sources: 6.0
+// us, 6.6 with two vectors a thread and the weights loaded where they are
+// used). With more rows than CUs the registers are worth more as occupancy
+// (16384 x 8192 over two sources: 222 against 234 us).
 template <int DT, bool TAIL, int NV, int WG>
 __global__ __launch_bounds__(WG) void k_norm(NormArgs a)
 {
     constexpr int VE = Elem<DT>::kVE, EB = Elem<DT>::kBytes;
+    constexpr bool kAhead = NV == 1;
     __shared__ float lds[2 * 16];
     int turn = 0;
     const size_t t = blockIdx.x;
-    const int hidden = (int)a.hidden;
-    float y[NV][VE];
-    fold_row<DT, TAIL, NV>(a.src, a.nsrc, t * a.ld_src * EB, hidden, y);
-    u32x4 res[NV];
+    const int hidden = (int)a.hidden, tid = (int)threadIdx.x, bd = (int)blockDim.x;
+    const char* grow = a.gate ? static_cast<const char*>(a.gate) + t / a.gate_rows * a.hidden * EB : nullptr;
+    u32x4 res[NV], wpost[NV], wpre[NV], gv[NV];
+    auto load = [&](u32x4* to, const void* row) {
+#pragma unroll
+        for (int u = 0; u < NV; ++u)
+            to[u] = ld_row<DT, TAIL>(row, tid + u * bd, hidden);
+    };
     if (a.residual)
 #pragma unroll
         for (int u = 0; u < NV; ++u)
-            res[u] = ld_row<DT, TAIL, true>(static_cast<const char*>(a.residual) + t * a.ld_residual * EB,
-                                            (int)threadIdx.x + u * (int)blockDim.x, hidden);
+            res[u] = ld_row<DT, TAIL, true>(static_cast<const char*>(a.residual) + t * a.ld_residual * EB, tid + u * bd, hidden);
+    if (kAhead) {
+        if (a.w_post) load(wpost, a.w_post);
+        if (grow) load(gv, grow);
+        if (a.out_z) load(wpre, a.w_pre);
+    }
+    float y[NV][VE];
+    fold_row<DT, TAIL, NV>(a.src, a.nsrc, t * a.ld_src * EB, hidden, y);
     if (a.w_post) {
         float s = 0.0f;
 #pragma unroll
@@ -51,23 +71,24 @@ __global__ __launch_bounds__(WG) void k_norm(NormArgs a)
                 s += y[u][k] * y[u][k];
         block_sums<1>(&s, lds, turn);
         const float p = 1.0f / __builtin_sqrtf(s * a.inv_hidden + a.eps);
-        if (a.rstd_post && threadIdx.x == 0)
+        if (a.rstd_post && tid == 0)
             a.rstd_post[t] = p;
+        if (!kAhead) load(wpost, a.w_post);
 #pragma unroll
         for (int u = 0; u < NV; ++u) {
             float w[VE];
-            unpack<DT>(ld_row<DT, TAIL>(a.w_post, (int)threadIdx.x + u * (int)blockDim.x, hidden), w);
+            unpack<DT>(wpost[u], w);
 #pragma unroll
             for (int k = 0; k < VE; ++k)
                 y[u][k] = y[u][k] * p * w[k];
         }
     }
-    if (a.gate) {
-        const char* grow = static_cast<const char*>(a.gate) + t / a.gate_rows * a.hidden * EB;
+    if (grow) {
+        if (!kAhead) load(gv, grow);
 #pragma unroll
         for (int u = 0; u < NV; ++u) {
             float g[VE];
-            unpack<DT>(ld_row<DT, TAIL>(grow, (int)threadIdx.x + u * (int)blockDim.x, hidden), g);
+            unpack<DT>(gv[u], g);
 #pragma unroll
             for (int k = 0; k < VE; ++k)
                 y[u][k] *= g[k];
@@ -86,8 +107,7 @@ __global__ __launch_bounds__(WG) void k_norm(NormArgs a)
     if (a.out_h) {
 #pragma unroll
         for (int u = 0; u < NV; ++u)
-            st_row<DT, TAIL, true>(static_cast<char*>(a.out_h) + t * a.ld_h * EB,
-                                   (int)threadIdx.x + u * (int)blockDim.x, hidden, pack<DT>(y[u]));
+            st_row<DT, TAIL, true>(static_cast<char*>(a.out_h) + t * a.ld_h * EB, tid + u * bd, hidden, pack<DT>(y[u]));
     }
     if (!a.out_z)
         return;
@@ -99,17 +119,17 @@ __global__ __launch_bounds__(WG) void k_norm(NormArgs a)
             s += y[u][k] * y[u][k];
     block_sums<1>(&s, lds, turn);
     const float q = 1.0f / __builtin_sqrtf(s * a.inv_hidden + a.eps);
-    if (a.rstd_pre && threadIdx.x == 0)
+    if (a.rstd_pre && tid == 0)
         a.rstd_pre[t] = q;
+    if (!kAhead) load(wpre, a.w_pre);
 #pragma unroll
     for (int u = 0; u < NV; ++u) {
         float w[VE];
-        unpack<DT>(ld_row<DT, TAIL>(a.w_pre, (int)threadIdx.x + u * (int)blockDim.x, hidden), w);
+        unpack<DT>(wpre[u], w);
 #pragma unroll
         for (int k = 0; k < VE; ++k)
             w[k] = y[u][k] * q * w[k];
-        st_row<DT, TAIL, true>(static_cast<char*>(a.out_z) + t * a.ld_z * EB,
-                               (int)threadIdx.x + u * (int)blockDim.x, hidden, pack<DT>(w));
+        st_row<DT, TAIL, true>(static_cast<char*>(a.out_z) + t * a.ld_z * EB, tid + u * bd, hidden, pack<DT>(w));
     }
 }
 
@@ -131,8 +151,14 @@ const void* norm_fn(int dtype, bool tail, unsigned wg, size_t nvec)
                      : norm_of<8, 1024>(dtype, tail);
 }
 
-// Two vectors a thread where up to 1024 threads allow it.
-unsigned norm_threads(size_t nvec) { return threads_for((nvec + 1) / 2, 1024); }
+// Two vectors a thread where up to 1024 threads allow it; one where there are
+// no more rows than CUs, for the latency. Whole waves only: a row of 1251
+// vectors takes 640 threads, three to a CU.
+unsigned norm_threads(size_t nvec, size_t rows)
+{
+    const size_t per = rows <= (size_t)device_cu_count() ? 1 : 2, t = (nvec + per - 1) / per;
+    return t >= 1024 ? 1024u : t < kWave ? (unsigned)kWave : (unsigned)((t + kWave - 1) / kWave * kWave);
+}
 
 }  // namespace
 
@@ -141,7 +167,7 @@ hipError_t launch_norm(const NormArgs& in, int dtype, hipStream_t s)
     NormArgs a = in;
     void* params[] = {&a};
     const size_t nvec = vectors(a.hidden, dtype);
-    const unsigned wg = norm_threads(nvec);
+    const unsigned wg = norm_threads(nvec, a.rows);
     return launch_logged("k_norm", norm_fn(dtype, partial(a.hidden, dtype), wg, nvec), dim3((unsigned)a.rows), dim3(wg),
                          params, s);
 }

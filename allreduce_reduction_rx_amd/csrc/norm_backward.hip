@@ -169,7 +169,8 @@ template <int DT, bool TAIL, int NV, int WG, int R, bool MULTI, bool ACC>
 __global__ __launch_bounds__(WG, WG > 512 ? 4 : 2) void k_norm_backward(NormBwdArgs a)
 {
     constexpr int VE = Elem<DT>::kVE, EB = Elem<DT>::kBytes, W = WG / R, E = NV * VE;
-    constexpr int PS = ACC ? 2 : 4;   // sources loaded ahead
+    constexpr int PS = ACC ? 2 : 4;   // sources loaded together with the rest
+    constexpr bool kAhead = WG <= 512;
     static_assert(R == 1 || W == kWave, "teams of several waves share no barriers");
     __shared__ float sums[2 * 16 * 3];
     __shared__ __align__(16) float dyn[ACC ? 2 * W * E : R > 1 ? R * W * VE : 4];
@@ -217,6 +218,11 @@ __global__ __launch_bounds__(WG, WG > 512 ? 4 : 2) void k_norm_backward(NormBwdA
             nq = a.rstd_pre[t];
     };
 
+    // one team: a part's rows follow each other; several: each gate row's
+    // first rows are loaded where they are needed
+    constexpr bool kRun = kAhead && R == 1;
+    if constexpr (kRun)
+        load(r0);
     size_t have = ~(size_t)0, grp = r0 / a.gate_rows;
     for (size_t s0 = r0; s0 < r1; ++grp) {
         const size_t ge = (grp + 1) * a.gate_rows;
@@ -226,7 +232,7 @@ __global__ __launch_bounds__(WG, WG > 512 ? 4 : 2) void k_norm_backward(NormBwdA
             for (int u = 0; u < NV; ++u)
                 gv[u] = ld_row<DT, TAIL>(static_cast<const char*>(a.gate) + grp * a.hidden * EB, tid + u * W, hidden);
         for (size_t t = s0 + team; t < s1; t += R) {
-            if (have != t)
+            if (!kRun && have != t)
                 load(t);
             const float p = np, q = nq;
             float y[NV][VE], h[NV][VE], e[NV][VE], s[3] = {0.0f, 0.0f, 0.0f};
@@ -256,7 +262,7 @@ __global__ __launch_bounds__(WG, WG > 512 ? 4 : 2) void k_norm_backward(NormBwdA
                 add_to<ACC, VE>(acc_pre + u * VE, lp + u * (VE / 4) * W, W, pre);
             }
             const size_t next = t + R < s1 ? t + R : R == 1 ? s1 : r1;
-            if (!ACC && next < r1) {
+            if (kAhead && next < r1) {
                 load(next);
                 have = next;
             }
@@ -277,6 +283,7 @@ __global__ __launch_bounds__(WG, WG > 512 ? 4 : 2) void k_norm_backward(NormBwdA
         if constexpr (MULTI) {
             // this gate row's rows of the part are done
             float* to = gate_target(a, grp, r0, r1);
+            float* post = a.part_post + blockIdx.x * a.hidden;
 #pragma unroll
             for (int u = 0; u < NV; ++u) {
                 float w1[VE], g[VE], tv[VE];
@@ -286,14 +293,14 @@ __global__ __launch_bounds__(WG, WG > 512 ? 4 : 2) void k_norm_backward(NormBwdA
                 join_teams<R, W, VE>(tv, team, tid, dyn);
 #pragma unroll
                 for (int k = 0; k < VE; ++k) {
-                    const int c = (tid + u * W) * VE + k;
-                    if (team == 0 && c < hidden) {
+                    const uint32_t c = (uint32_t)((tid + u * W) * VE + k);
+                    if (team == 0 && c < (uint32_t)hidden) {
                         if (a.d_gate)
                             to[c] = w1[k] * tv[k];
-                        float* post = a.part_post + blockIdx.x * a.hidden + c;
-                        *post = s0 == r0 ? g[k] * tv[k] : *post + g[k] * tv[k];
+                        post[c] = s0 == r0 ? g[k] * tv[k] : post[c] + g[k] * tv[k];
                     }
                 }
+                __builtin_amdgcn_sched_barrier(0);   // one vector at a time: registers
             }
         }
         s0 = s1;
@@ -483,7 +490,7 @@ const void* backward_fn(unsigned threads, unsigned teams, int nv, bool multi)
     if (threads == 256)
         return backward_of<DT, TAIL, 2, 256, 1, false>(multi);
     if (threads == 512)
-        return backward_of<DT, TAIL, 2, 512, 1, false>(multi);
+        return nv <= 2 ? backward_of<DT, TAIL, 2, 512, 1, false>(multi) : backward_of<DT, TAIL, 3, 512, 1, DT == 1>(multi);
     if (nv <= 2)
         return backward_of<DT, TAIL, 2, 1024, 1, true>(multi);
     return multi ? (const void*)k_norm_backward_long<DT, TAIL, true> : (const void*)k_norm_backward_long<DT, TAIL, false>;
@@ -506,7 +513,7 @@ Spread spread(size_t rows, size_t hidden, size_t gate_rows, int dtype)
 {
     Spread s;
     const size_t nvec = vectors(hidden, dtype);
-    s.threads = threads_for((nvec + 1) / 2, 1024);
+    s.threads = nvec > 1024 && nvec <= 1536 ? 512 : threads_for((nvec + 1) / 2, 1024);
     s.nv = (int)((nvec + s.threads - 1) / s.threads);
     s.teams = s.threads == kWave && gate_rows >= 8 ? 8 : 1;
     const size_t wg = s.threads * s.teams;

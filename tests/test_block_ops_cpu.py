@@ -161,6 +161,29 @@ def test_binding_refuses_cpu_tensors(monkeypatch):
         rx.rx_moe_combine(x, torch.zeros(2, 2, dtype=torch.int32), None, torch.zeros(2, 8))
 
 
+def test_binding_refuses_what_is_no_matrix(monkeypatch):
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    x, i = torch.zeros(4, 8), torch.zeros(4, 2, dtype=torch.int32)
+    with pytest.raises(TypeError, match="x must be a tensor"):
+        rx.rx_quant_i8(5, x, x)
+    with pytest.raises(ValueError, match="two dimensions"):
+        rx.rx_quant_i8(torch.zeros(2, 3, 4), x, x)
+    with pytest.raises(TypeError, match="float32 or bfloat16"):
+        rx.rx_quant_i8(i, x, x)
+    with pytest.raises(ValueError, match="1 to 16 sources"):
+        rx.rx_residual_norm([], x, None, None, None, x, None)
+    with pytest.raises(ValueError, match="1 to 16 sources"):
+        rx.rx_residual_norm([x] * 17, x, None, None, None, x, None)
+    with pytest.raises(TypeError, match="sequence"):
+        rx.rx_residual_norm(3, x, None, None, None, x, None)
+    with pytest.raises(ValueError, match="b must have three dimensions"):
+        rx.rx_gemm_i8(x, x, x, x, x, offsets=i)
+    with pytest.raises(ValueError, match="32 bits"):
+        rx.rx_moe_dispatch(i, 1 << 40, i, i, i)
+    with pytest.raises(TypeError):
+        rx.rx_moe_dispatch(i, "eight", i, i, i)
+
+
 @pytest.mark.parametrize("post", [True, False])
 @pytest.mark.parametrize("gate_rows", [0, 2, 5])
 def test_reference_norm_gradient_against_differences(post, gate_rows):

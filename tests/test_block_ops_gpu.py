@@ -500,6 +500,32 @@ def test_gemm_offsets_outside_the_rows_are_clamped():
     out.check()
 
 
+def test_binding_refusals():
+    z = lambda *s, dtype=FP32: torch.zeros(*s, dtype=dtype, device="cuda")
+    x, codes, scales = z(4, 32), z(4, 32, dtype=torch.int8), z(4)
+    refused = [
+        (ValueError, "shape", lambda: rx.rx_quant_i8(x, z(4, 31, dtype=torch.int8), scales)),
+        (TypeError, "Char", lambda: rx.rx_quant_i8(x, x, scales)),
+        (ValueError, "rows must be contiguous", lambda: rx.rx_quant_i8(z(32, 4).t(), codes, scales)),
+        (ValueError, "overlap", lambda: rx.rx_quant_i8(torch.as_strided(z(64), (4, 32), (8, 1)), codes, scales)),
+        (ValueError, "scales must be contiguous", lambda: rx.rx_quant_i8(x, codes, z(8)[::2])),
+        (ValueError, "GPU tensor", lambda: rx.rx_quant_i8(x, codes, scales.cpu())),
+        (ValueError, "come together", lambda: rx.rx_moe_dispatch(z(4, 1, dtype=torch.int32), 2, z(3, dtype=torch.int32), z(4, dtype=torch.int32),
+                                                                 z(4, 1, dtype=torch.int32), x=x)),
+        (ValueError, "scales come with", lambda: rx.rx_moe_dispatch(z(4, 1, dtype=torch.int32), 2, z(3, dtype=torch.int32), z(4, dtype=torch.int32),
+                                                                    z(4, 1, dtype=torch.int32), x=x, rows=codes)),
+        (ValueError, "d_weights needs rows", lambda: rx.rx_moe_combine_backward(x, None, z(4, 1, dtype=torch.int32), None, z(3, dtype=torch.int32), x, z(4, 1))),
+        (ValueError, "another row stride", lambda: rx.rx_residual_norm([x, z(4, 40)[:, :32]], None, None, None, None, x, None)),
+        (ValueError, "gate_rows", lambda: rx.rx_residual_norm([x], None, z(1, 32), None, None, z(4, 32), None, gate_rows=0)),
+        (ValueError, "padded", lambda: rx.rx_gemm_i8(torch.as_strided(z(3 * 48 + 40, dtype=torch.int8), (4, 40), (48, 1)), scales, z(8, 48, dtype=torch.int8)[:, :40],
+                                                     z(8), z(4, 8))),
+        (rx.RxError, "RX_ERR_ARG", lambda: rx.rx_residual_norm([x], None, None, None, None, z(4, 32), None, eps=0.0)),
+    ]
+    for error, match, call in refused:
+        with pytest.raises(error, match=match):
+            call()
+
+
 # ---- far offsets, streams, graphs ------------------------------------------------
 
 def test_row_offsets_past_32_bits():

@@ -19,6 +19,10 @@ template <> struct Elem<1> { static constexpr int kVE = 8, kBytes = 2; };  // BF
 // take any address, so rows of odd length need no kernel of their own.
 typedef uint32_t u32x4_any __attribute__((ext_vector_type(4), aligned(2)));
 
+typedef uint32_t u32x2_any __attribute__((ext_vector_type(2), aligned(1)));
+typedef uint32_t u32_any __attribute__((aligned(1)));
+typedef uint16_t u16_any __attribute__((aligned(1)));
+
 __device__ __forceinline__ u32x4 ld16_any(const void* p)
 {
     return *reinterpret_cast<const u32x4_any*>(p);
@@ -41,32 +45,55 @@ __device__ __forceinline__ void st16_any_stream(void* p, u32x4 v)
 // the row are 0. Without TAIL hidden is a multiple of the vector. A row is
 // shorter than 2^32 bytes: with a uniform row pointer the 32-bit offset lets
 // the address stay in scalar registers.
+//
+// A partial vector is the last whole one of the row, shifted: one load, where
+// one for every element would be a chain of up to seven. ld_raw loads and
+// fixed() shifts: between the two go the other loads, so that none waits.
 template <int DT, bool TAIL, bool NT = false>
-__device__ __forceinline__ u32x4 ld_row(const void* row, int v, int hidden)
+__device__ __forceinline__ u32x4 ld_raw(const void* row, int v, int hidden)
 {
     constexpr int VE = Elem<DT>::kVE;
     const int c = v * VE;
+    const char* p = static_cast<const char*>(row);
     u32x4 x = {0, 0, 0, 0};
-    if (!TAIL || c + VE <= hidden) {
-        if (TAIL || c < hidden)
-            x = NT ? ld16_any_stream(static_cast<const char*>(row) + (uint32_t)c * (uint32_t)Elem<DT>::kBytes)
-                   : ld16_any(static_cast<const char*>(row) + (uint32_t)c * (uint32_t)Elem<DT>::kBytes);
-    } else if (c < hidden) {
-        const int n = hidden - c;   // 1 .. VE - 1
-        if constexpr (DT == 0) {
-            const uint32_t* p = static_cast<const uint32_t*>(row) + c;
-            x[0] = p[0];
-            if (n > 1) x[1] = p[1];
-            if (n > 2) x[2] = p[2];
-        } else {
-            const uint16_t* p = static_cast<const uint16_t*>(row) + c;
-#pragma unroll
-            for (int e = 0; e < VE - 1; ++e)
-                if (e < n)
-                    x[e / 2] |= (uint32_t)p[e] << (16 * (e & 1));
+    if (!TAIL || hidden >= VE) {
+        const int at = !TAIL || c < hidden - VE ? c : hidden - VE;
+        if (TAIL || c < hidden) {
+            p += (uint32_t)at * (uint32_t)Elem<DT>::kBytes;
+            x = NT ? ld16_any_stream(p) : ld16_any(p);
         }
+    } else if (c < hidden) {   // a row shorter than a vector
+#pragma unroll
+        for (int e = 0; e < VE - 1; ++e)
+            if (e < hidden) {
+                if constexpr (DT == 0)
+                    x[e] = reinterpret_cast<const uint32_t*>(p)[e];
+                else
+                    x[e / 2] |= (uint32_t) reinterpret_cast<const uint16_t*>(p)[e] << (16 * (e & 1));
+            }
     }
     return x;
+}
+
+template <int DT, bool TAIL>
+__device__ __forceinline__ u32x4 fixed(u32x4 x, int v, int hidden)
+{
+    constexpr int VE = Elem<DT>::kVE;
+    const int d = v * VE + VE - hidden;   // elements past the row
+    if (TAIL && d > 0 && hidden >= VE) {
+        const uint64_t lo = x[0] | (uint64_t)x[1] << 32, hi = x[2] | (uint64_t)x[3] << 32;
+        const int s = d * Elem<DT>::kBytes * 8;   // bits
+        const uint64_t l = s < 64 ? lo >> s | hi << (64 - s) : s < 128 ? hi >> (s - 64) : 0;
+        const uint64_t h = s < 64 ? hi >> s : 0;
+        x = u32x4{(uint32_t)l, (uint32_t)(l >> 32), (uint32_t)h, (uint32_t)(h >> 32)};
+    }
+    return x;
+}
+
+template <int DT, bool TAIL, bool NT = false>
+__device__ __forceinline__ u32x4 ld_row(const void* row, int v, int hidden)
+{
+    return fixed<DT, TAIL>(ld_raw<DT, TAIL, NT>(row, v, hidden), v, hidden);
 }
 
 template <int DT, bool TAIL, bool NT = false>
@@ -74,25 +101,26 @@ __device__ __forceinline__ void st_row(void* row, int v, int hidden, u32x4 x)
 {
     constexpr int VE = Elem<DT>::kVE;
     const int c = v * VE;
+    char* p = static_cast<char*>(row) + (uint32_t)c * (uint32_t)Elem<DT>::kBytes;
     if (!TAIL || c + VE <= hidden) {
         if (TAIL || c < hidden) {
-            char* p = static_cast<char*>(row) + (uint32_t)c * (uint32_t)Elem<DT>::kBytes;
             if (NT) st16_any_stream(p, x); else st16_any(p, x);
         }
     } else if (c < hidden) {
-        const int n = hidden - c;
-        if constexpr (DT == 0) {
-            uint32_t* p = static_cast<uint32_t*>(row) + c;
-            p[0] = x[0];
-            if (n > 1) p[1] = x[1];
-            if (n > 2) p[2] = x[2];
-        } else {
-            uint16_t* p = static_cast<uint16_t*>(row) + c;
-#pragma unroll
-            for (int e = 0; e < VE - 1; ++e)
-                if (e < n)
-                    p[e] = (uint16_t)(x[e / 2] >> (16 * (e & 1)));
+        const int n = (hidden - c) * Elem<DT>::kBytes;   // bytes
+        if (n & 8) {
+            *reinterpret_cast<u32x2_any*>(p) = (u32x2_any){x[0], x[1]};
+            x[0] = x[2];
+            x[1] = x[3];
+            p += 8;
         }
+        if (n & 4) {
+            *reinterpret_cast<u32_any*>(p) = x[0];
+            x[0] = x[1];
+            p += 4;
+        }
+        if (DT != 0 && (n & 2))
+            *reinterpret_cast<uint16_t*>(p) = (uint16_t)x[0];
     }
 }
 
@@ -215,9 +243,6 @@ __device__ __forceinline__ void i8_codes(u32x4 x, float r, uint32_t* q)
     }
 }
 
-typedef uint32_t u32x2_any __attribute__((ext_vector_type(2), aligned(1)));
-typedef uint32_t u32_any __attribute__((aligned(1)));
-
 // Vector v's codes into a row of `hidden` bytes.
 template <int DT, bool TAIL>
 __device__ __forceinline__ void st_codes(void* row, int v, int hidden, const uint32_t* q)
@@ -233,10 +258,20 @@ __device__ __forceinline__ void st_codes(void* row, int v, int hidden, const uin
                 *reinterpret_cast<u32_any*>(p) = q[0];
         }
     } else if (c < hidden) {
-#pragma unroll
-        for (int e = 0; e < VE - 1; ++e)
-            if (c + e < hidden)
-                p[e] = (uint8_t)(q[e / 4] >> (8 * (e & 3)));
+        const int n = hidden - c;
+        uint32_t w = q[0];
+        if (VE == 8 && (n & 4)) {
+            *reinterpret_cast<u32_any*>(p) = w;
+            w = q[VE / 4 - 1];
+            p += 4;
+        }
+        if (n & 2) {
+            *reinterpret_cast<u16_any*>(p) = (uint16_t)w;
+            w >>= 16;
+            p += 2;
+        }
+        if (n & 1)
+            *p = (uint8_t)w;
     }
 }
 

@@ -24,7 +24,10 @@ __global__ __launch_bounds__(256) void k_quant_i8(QuantI8Args a)
     u32x4 x[NV];
 #pragma unroll
     for (int u = 0; u < NV; ++u)
-        x[u] = ld_row<DT, TAIL, true>(row, tid + u * bd, k);
+        x[u] = ld_raw<DT, TAIL, true>(row, tid + u * bd, k);
+#pragma unroll
+    for (int u = 0; u < NV; ++u)
+        x[u] = fixed<DT, TAIL>(x[u], tid + u * bd, k);
     uint32_t m = 0;
 #pragma unroll
     for (int u = 0; u < NV; ++u)

@@ -196,7 +196,10 @@ __global__ __launch_bounds__(256) void k_dispatch_rows(DispatchArgs a)
     auto load = [&](int base) {
 #pragma unroll
         for (int u = 0; u < NV; ++u)
-            x[u] = ld_row<DT, TAIL, OUT == 1>(xrow, base + u * bd, hidden);
+            x[u] = ld_raw<DT, TAIL, OUT == 1>(xrow, base + u * bd, hidden);
+#pragma unroll
+        for (int u = 0; u < NV; ++u)
+            x[u] = fixed<DT, TAIL>(x[u], base + u * bd, hidden);
     };
     load(v0 + tid);
     float scale = 1.0f, inv = 1.0f;
@@ -420,14 +423,14 @@ __device__ __forceinline__ void combine_batch(const CombineArgs& a, uint64_t& ma
         const char* row = static_cast<const char*>(a.rows) + (size_t)s * a.ld_rows * Elem<DT>::kBytes;
 #pragma unroll
         for (int u = 0; u < U; ++u)
-            x[r][u] = ld_row<DT, TAIL, true>(row, v + u * kWave, hidden);
+            x[r][u] = ld_raw<DT, TAIL, true>(row, v + u * kWave, hidden);
     }
 #pragma unroll
     for (int r = 0; r < N; ++r)
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             float f[VE];
-            unpack<DT>(x[r][u], f);
+            unpack<DT>(fixed<DT, TAIL>(x[r][u], v + u * kWave, hidden), f);
 #pragma unroll
             for (int k = 0; k < VE; ++k)
                 acc[u][k] += ws[r] * f[k];
@@ -502,11 +505,11 @@ __global__ __launch_bounds__(256) void k_combine_backward(CombineBwdArgs a)
                     u32x4 x[NV];
 #pragma unroll
                     for (int u = 0; u < NV; ++u)
-                        x[u] = ld_row<DT, TAIL, true>(row, base + u * bd, hidden);
+                        x[u] = ld_raw<DT, TAIL, true>(row, base + u * bd, hidden);
 #pragma unroll
                     for (int u = 0; u < NV; ++u) {
                         float f[VE];
-                        unpack<DT>(x[u], f);
+                        unpack<DT>(fixed<DT, TAIL>(x[u], base + u * bd, hidden), f);
 #pragma unroll
                         for (int k = 0; k < VE; ++k)
                             dot[j] += g[u][k] * f[k];

@@ -49,12 +49,12 @@ __global__ __launch_bounds__(WG) void k_norm(NormArgs a)
     auto load = [&](u32x4* to, const void* row) {
 #pragma unroll
         for (int u = 0; u < NV; ++u)
-            to[u] = ld_row<DT, TAIL>(row, tid + u * bd, hidden);
+            to[u] = ld_raw<DT, TAIL>(row, tid + u * bd, hidden);
     };
     if (a.residual)
 #pragma unroll
         for (int u = 0; u < NV; ++u)
-            res[u] = ld_row<DT, TAIL, true>(static_cast<const char*>(a.residual) + t * a.ld_residual * EB, tid + u * bd, hidden);
+            res[u] = ld_raw<DT, TAIL, true>(static_cast<const char*>(a.residual) + t * a.ld_residual * EB, tid + u * bd, hidden);
     if (kAhead) {
         if (a.w_post) load(wpost, a.w_post);
         if (grow) load(gv, grow);
@@ -77,7 +77,7 @@ __global__ __launch_bounds__(WG) void k_norm(NormArgs a)
 #pragma unroll
         for (int u = 0; u < NV; ++u) {
             float w[VE];
-            unpack<DT>(wpost[u], w);
+            unpack<DT>(fixed<DT, TAIL>(wpost[u], tid + u * bd, hidden), w);
 #pragma unroll
             for (int k = 0; k < VE; ++k)
                 y[u][k] = y[u][k] * p * w[k];
@@ -88,7 +88,7 @@ __global__ __launch_bounds__(WG) void k_norm(NormArgs a)
 #pragma unroll
         for (int u = 0; u < NV; ++u) {
             float g[VE];
-            unpack<DT>(gv[u], g);
+            unpack<DT>(fixed<DT, TAIL>(gv[u], tid + u * bd, hidden), g);
 #pragma unroll
             for (int k = 0; k < VE; ++k)
                 y[u][k] *= g[k];
@@ -98,7 +98,7 @@ __global__ __launch_bounds__(WG) void k_norm(NormArgs a)
 #pragma unroll
         for (int u = 0; u < NV; ++u) {
             float f[VE];
-            unpack<DT>(res[u], f);
+            unpack<DT>(fixed<DT, TAIL>(res[u], tid + u * bd, hidden), f);
 #pragma unroll
             for (int k = 0; k < VE; ++k)
                 y[u][k] += a.residual_scale * f[k];
@@ -125,7 +125,7 @@ __global__ __launch_bounds__(WG) void k_norm(NormArgs a)
 #pragma unroll
     for (int u = 0; u < NV; ++u) {
         float w[VE];
-        unpack<DT>(wpre[u], w);
+        unpack<DT>(fixed<DT, TAIL>(wpre[u], tid + u * bd, hidden), w);
 #pragma unroll
         for (int k = 0; k < VE; ++k)
             w[k] = y[u][k] * q * w[k];

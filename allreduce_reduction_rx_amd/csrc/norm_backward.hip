@@ -207,10 +207,10 @@ __global__ __launch_bounds__(WG, WG > 512 ? 4 : 2) void k_norm_backward(NormBwdA
 #pragma unroll
             for (int r = 0; r < PS; ++r)
                 if (r < a.nsrc)
-                    src[r][u] = ld_row<DT, TAIL, true>(static_cast<const char*>(a.src[r]) + t * a.ld_src * EB, v, hidden);
-            res[u] = a.residual ? ld_row<DT, TAIL, true>(static_cast<const char*>(a.residual) + t * a.ld_residual * EB, v, hidden) : zero;
-            dhv[u] = a.d_h ? ld_row<DT, TAIL, true>(static_cast<const char*>(a.d_h) + t * a.ld_d_h * EB, v, hidden) : zero;
-            dzv[u] = a.d_z ? ld_row<DT, TAIL, true>(static_cast<const char*>(a.d_z) + t * a.ld_d_z * EB, v, hidden) : zero;
+                    src[r][u] = ld_raw<DT, TAIL, true>(static_cast<const char*>(a.src[r]) + t * a.ld_src * EB, v, hidden);
+            res[u] = a.residual ? ld_raw<DT, TAIL, true>(static_cast<const char*>(a.residual) + t * a.ld_residual * EB, v, hidden) : zero;
+            dhv[u] = a.d_h ? ld_raw<DT, TAIL, true>(static_cast<const char*>(a.d_h) + t * a.ld_d_h * EB, v, hidden) : zero;
+            dzv[u] = a.d_z ? ld_raw<DT, TAIL, true>(static_cast<const char*>(a.d_z) + t * a.ld_d_z * EB, v, hidden) : zero;
         }
         if (a.w_post)
             np = a.rstd_post[t];
@@ -238,12 +238,12 @@ __global__ __launch_bounds__(WG, WG > 512 ? 4 : 2) void k_norm_backward(NormBwdA
             float y[NV][VE], h[NV][VE], e[NV][VE], s[3] = {0.0f, 0.0f, 0.0f};
 #pragma unroll
             for (int u = 0; u < NV; ++u) {
-                unpack<DT>(src[0][u], y[u]);
+                unpack<DT>(fixed<DT, TAIL>(src[0][u], tid + u * W, hidden), y[u]);
 #pragma unroll
                 for (int r = 1; r < PS; ++r)
                     if (r < a.nsrc) {
                         float f[VE];
-                        unpack<DT>(src[r][u], f);
+                        unpack<DT>(fixed<DT, TAIL>(src[r][u], tid + u * W, hidden), f);
 #pragma unroll
                         for (int k = 0; k < VE; ++k)
                             y[u][k] += f[k];
@@ -257,7 +257,8 @@ __global__ __launch_bounds__(WG, WG > 512 ? 4 : 2) void k_norm_backward(NormBwdA
 #pragma unroll
             for (int u = 0; u < NV; ++u) {
                 float pre[VE];
-                row_sums<DT, VE>(y[u], res[u], dhv[u], dzv[u], held(wpost[u]), held(wpre[u]), held(gv[u]), p, q,
+                auto whole = [&](u32x4 x) { return fixed<DT, TAIL>(x, tid + u * W, hidden); };
+                row_sums<DT, VE>(y[u], whole(res[u]), whole(dhv[u]), whole(dzv[u]), held(wpost[u]), held(wpre[u]), held(gv[u]), p, q,
                                  a.residual_scale, h[u], e[u], pre, s);
                 add_to<ACC, VE>(acc_pre + u * VE, lp + u * (VE / 4) * W, W, pre);
             }

@@ -48,13 +48,13 @@ __device__ __forceinline__ void fold_batch(const void* const* src, int r, size_t
     for (int b = 0; b < B; ++b)
 #pragma unroll
         for (int u = 0; u < NV; ++u)
-            x[b][u] = ld_row<DT, TAIL, true>(static_cast<const char*>(src[r + b]) + row_bytes, tid + u * threads, hidden);
+            x[b][u] = ld_raw<DT, TAIL, true>(static_cast<const char*>(src[r + b]) + row_bytes, tid + u * threads, hidden);
 #pragma unroll
     for (int b = 0; b < B; ++b)
 #pragma unroll
         for (int u = 0; u < NV; ++u) {
             float f[VE];
-            unpack<DT>(x[b][u], f);
+            unpack<DT>(fixed<DT, TAIL>(x[b][u], tid + u * threads, hidden), f);
 #pragma unroll
             for (int k = 0; k < VE; ++k)
                 y[u][k] = FIRST && b == 0 ? f[k] : y[u][k] + f[k];

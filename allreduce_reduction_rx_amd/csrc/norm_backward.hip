@@ -106,6 +106,34 @@ __device__ __forceinline__ u32x4 ones(int dt)
     return u32x4{o, o, o, o};
 }
 
+// N floats of a row of sums from column c on, and back.
+template <int N>
+__device__ __forceinline__ void st_sums(float* row, uint32_t c, uint32_t hidden, const float* x)
+{
+    if (c + N <= hidden) {
+#pragma unroll
+        for (int k = 0; k < N; k += 4)
+            st16_any(row + c + k, pack<0>(x + k));
+    } else {
+#pragma unroll
+        for (int k = 0; k < N; ++k)
+            if (c + k < hidden)
+                row[c + k] = x[k];
+    }
+}
+template <int N>
+__device__ __forceinline__ void ld_sums(const float* row, uint32_t c, uint32_t hidden, float* x)
+{
+#pragma unroll
+    for (int k = 0; k < N; k += 4)
+        if (c + N <= hidden)
+            unpack<0>(ld16_any(row + c + k), x + k);
+        else
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                x[k + i] = c + k + i < hidden ? row[c + k + i] : 0.0f;
+}
+
 // One vector of a row up to the three sums: h, e, and d_w_pre's term.
 template <int DT, int VE>
 __device__ __forceinline__ void row_sums(const float* y, u32x4 res, u32x4 dhv, u32x4 dzv, u32x4 wpost, u32x4 wpre,
@@ -292,14 +320,19 @@ __global__ __launch_bounds__(WG, WG > 512 ? 4 : 2) void k_norm_backward(NormBwdA
                 unpack<DT>(held(gv[u]), g);
                 take<ACC, VE>(acc_t + u * VE, lt + u * (VE / 4) * W, W, tv);
                 join_teams<R, W, VE>(tv, team, tid, dyn);
+                const uint32_t c = (uint32_t)((tid + u * W) * VE);
+                if (team == 0 && c < (uint32_t)hidden) {
+                    float sum[VE];
+                    if (s0 > r0)
+                        ld_sums<VE>(post, c, hidden, sum);
 #pragma unroll
-                for (int k = 0; k < VE; ++k) {
-                    const uint32_t c = (uint32_t)((tid + u * W) * VE + k);
-                    if (team == 0 && c < (uint32_t)hidden) {
-                        if (a.d_gate)
-                            to[c] = w1[k] * tv[k];
-                        post[c] = s0 == r0 ? g[k] * tv[k] : post[c] + g[k] * tv[k];
+                    for (int k = 0; k < VE; ++k) {
+                        sum[k] = s0 == r0 ? g[k] * tv[k] : sum[k] + g[k] * tv[k];
+                        tv[k] *= w1[k];
                     }
+                    st_sums<VE>(post, c, hidden, sum);
+                    if (a.d_gate)
+                        st_sums<VE>(to, c, hidden, tv);
                 }
                 __builtin_amdgcn_sched_barrier(0);   // one vector at a time: registers
             }
@@ -315,14 +348,11 @@ __global__ __launch_bounds__(WG, WG > 512 ? 4 : 2) void k_norm_backward(NormBwdA
         }
         take<ACC, VE>(acc_pre + u * VE, lp + u * (VE / 4) * W, W, pre);
         join_teams<R, W, VE>(pre, team, tid, dyn);
-#pragma unroll
-        for (int k = 0; k < VE; ++k) {
-            const int c = (tid + u * W) * VE + k;
-            if (team == 0 && c < hidden) {
-                if constexpr (!MULTI)
-                    a.part_post[blockIdx.x * a.hidden + c] = tv[k];
-                a.part_pre[blockIdx.x * a.hidden + c] = pre[k];
-            }
+        const uint32_t c = (uint32_t)((tid + u * W) * VE);
+        if (team == 0 && c < (uint32_t)hidden) {
+            if constexpr (!MULTI)
+                st_sums<VE>(a.part_post + blockIdx.x * a.hidden, c, hidden, tv);
+            st_sums<VE>(a.part_pre + blockIdx.x * a.hidden, c, hidden, pre);
         }
     }
 }
@@ -380,14 +410,18 @@ __global__ __launch_bounds__(1024) void k_norm_backward_long(NormBwdArgs a)
                     if (a.d_residual)
                         st_row<DT, TAIL>(static_cast<char*>(a.d_residual) + t * a.ld_d_residual * EB, v, hidden, pack<DT>(o1));
                     st_row<DT, TAIL>(static_cast<char*>(a.d_src) + t * a.ld_d_src * EB, v, hidden, pack<DT>(o2));
+                    float ot[VE] = {}, op[VE] = {};
+                    if (t > s0)
+                        ld_sums<VE>(to, v * VE, hidden, ot);
+                    if (t > r0)
+                        ld_sums<VE>(part_pre, v * VE, hidden, op);
 #pragma unroll
                     for (int k = 0; k < VE; ++k) {
-                        const int c = v * VE + k;
-                        if (c < hidden) {
-                            to[c] = t == s0 ? tt[k] : to[c] + tt[k];
-                            part_pre[c] = t == r0 ? pre[k] : part_pre[c] + pre[k];
-                        }
+                        ot[k] += tt[k];
+                        op[k] += pre[k];
                     }
+                    st_sums<VE>(to, v * VE, hidden, ot);
+                    st_sums<VE>(part_pre, v * VE, hidden, op);
                 }
                 if (pass == 0) {
                     block_sums<3, 1024 / kWave>(s, sums, turn);

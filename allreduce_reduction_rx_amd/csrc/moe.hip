@@ -269,12 +269,40 @@ __global__ __launch_bounds__(256) void k_dispatch_rows(DispatchArgs a)
     }
 }
 
-// Plan and rows in one launch. OUT 0: the plan alone; 1: rows copied; 2: rows
-// quantized to INT8.
+// Plan and rows in one launch, up to kDispatchCountAll pairs. OUT 0: the plan
+// alone; 1: rows copied; 2: rows quantized to INT8.
+//
+// A pair's place is the number of (expert, pair) keys below its own: one
+// comparison and one addition of a carry for an id. The loop over the ids stays
+// rolled: at these sizes a kernel's time is its way through code that no
+// instruction cache holds yet (16 ids at a time, unrolled: 8.4 us where 32
+// tokens take 6.2).
+constexpr int kPairBits = 12;
+static_assert(kDispatchCountAll <= 1 << kPairBits, "a key holds the pair's number");
+
+__device__ __forceinline__ uint32_t pair_key(int expert, uint32_t pair) { return (uint32_t)expert << kPairBits | pair; }
+
+// c[j] = the thread's ids whose keys are below to[j].
+template <int N>
+__device__ __forceinline__ void count_below(const DispatchArgs& a, const uint32_t* to, uint32_t* c)
+{
+#pragma unroll
+    for (int j = 0; j < N; ++j)
+        c[j] = 0;
+#pragma unroll 1
+    for (uint32_t i = threadIdx.x; i < a.pairs; i += blockDim.x) {
+        const uint32_t key = pair_key(local_expert(a.ids[i], a.first, a.experts), i);
+#pragma unroll
+        for (int j = 0; j < N; ++j)
+            c[j] += key < to[j];
+    }
+}
+
 template <int DT, int OUT, bool TAIL>
 __global__ __launch_bounds__(256) void k_dispatch(DispatchArgs a)
 {
     __shared__ uint32_t lds[4 * (kGroup + 1)];
+    __shared__ uint32_t tops[4];
     const int tid = threadIdx.x, bd = blockDim.x;
     const uint32_t t = blockIdx.x;
 
@@ -283,13 +311,11 @@ __global__ __launch_bounds__(256) void k_dispatch(DispatchArgs a)
         if (blockIdx.y)
             return;
         const int e0 = (int)(t - a.tokens) * kGroup;
-        uint32_t c[kGroup] = {};
-        for (uint32_t i = tid; i < a.pairs; i += bd) {
-            const int e = local_expert(a.ids[i], a.first, a.experts);
+        uint32_t c[kGroup], to[kGroup];
 #pragma unroll
-            for (int j = 0; j < kGroup; ++j)
-                c[j] += e < e0 + j;
-        }
+        for (int j = 0; j < kGroup; ++j)
+            to[j] = pair_key(e0 + j < a.experts ? e0 + j : a.experts, 0);
+        count_below<kGroup>(a, to, c);
         block_counts<kGroup>(c, lds);
 #pragma unroll
         for (int j = 0; j < kGroup; ++j)
@@ -299,49 +325,51 @@ __global__ __launch_bounds__(256) void k_dispatch(DispatchArgs a)
     }
 
     const void* xrow = static_cast<const char*>(a.x) + (size_t)t * a.ld_x * Elem<DT>::kBytes;
-    constexpr int VE = Elem<DT>::kVE;
+    constexpr int VE = Elem<DT>::kVE, XN = OUT == 2 ? 2 : 1;
     const int hidden = (int)a.hidden;
     const int nvec = (hidden + VE - 1) / VE;
     const int v0 = (int)(blockIdx.y * a.split_vecs);
     const int v1 = v0 + (int)a.split_vecs < nvec ? v0 + (int)a.split_vecs : nvec;
+    u32x4 x[XN];
+    if constexpr (OUT != 0)
+#pragma unroll
+        for (int u = 0; u < XN; ++u)
+            x[u] = ld_raw<DT, TAIL>(xrow, v0 + tid + u * bd, hidden);
 
     float scale = 1.0f, inv = 1.0f;
-    if constexpr (OUT == 2) {
-        uint32_t m = 0;
-        for (int v = tid; v < nvec; v += bd)
-            m = umax(m, vec_absmax<DT>(ld_row<DT, TAIL>(xrow, v, hidden)));
-        m = group_max<kWave>(m);
-        if (bd > kWave) {
-            if (lane_id() == 0)
-                lds[tid / kWave] = m;
-            __syncthreads();
-            for (int w = 0; w < bd / kWave; ++w)
-                m = umax(m, lds[w]);
-        }
-        i8_scale(bits_f32(m), scale, inv);
-    }
-
-    u32x4 x0;   // on its way while the pairs are counted
-    if constexpr (OUT != 0)
-        x0 = ld_row<DT, TAIL>(xrow, v0 + tid, hidden);
     uint32_t kept = 0;
     for (int j0 = 0; j0 < a.topk; j0 += kGroup) {
         const int nj = a.topk - j0 < kGroup ? a.topk - j0 : kGroup;
         const uint32_t i0 = t * (uint32_t)a.topk + (uint32_t)j0;
         int key[kGroup];
+        uint32_t c[kGroup + 1], to[kGroup + 1];
 #pragma unroll
-        for (int j = 0; j < kGroup; ++j)
+        for (int j = 0; j < kGroup; ++j) {
             key[j] = j < nj ? local_expert(a.ids[i0 + j], a.first, a.experts) : a.experts;
-        uint32_t c[kGroup + 1] = {};
-        for (uint32_t i = tid; i < a.pairs; i += bd) {
-            const int e = local_expert(a.ids[i], a.first, a.experts);
-            c[kGroup] += e < a.experts;
-#pragma unroll
-            for (int j = 0; j < kGroup; ++j)
-                c[j] += e < key[j] || (e == key[j] && i < i0 + j);
+            to[j] = pair_key(key[j], i0 + j);
         }
-        block_counts<kGroup + 1>(c, lds);
+        to[kGroup] = pair_key(a.experts, 0);   // all that are kept
+        count_below<kGroup + 1>(a, to, c);
+        if (OUT == 2 && j0 == 0) {
+            uint32_t m = 0;
+#pragma unroll
+            for (int u = 0; u < XN; ++u)
+                m = umax(m, vec_absmax<DT>(fixed<DT, TAIL>(x[u], v0 + tid + u * bd, hidden)));
+            for (int v = tid; v < nvec; v += bd)   // the rest, and the other parts of a split row
+                if (v < v0 || v >= v0 + XN * bd)
+                    m = umax(m, vec_absmax<DT>(ld_row<DT, TAIL>(xrow, v, hidden)));
+            m = group_max<kWave>(m);
+            if (lane_id() == 0)
+                tops[tid / kWave] = m;
+        }
+        block_counts<kGroup + 1>(c, lds);   // with several waves: barriers after tops is written
         kept = c[kGroup];
+        if (OUT == 2 && j0 == 0) {
+            uint32_t m = tops[0];
+            for (int w = 1; w < bd / kWave; ++w)
+                m = umax(m, tops[w]);
+            i8_scale(bits_f32(m), scale, inv);
+        }
         if (blockIdx.y == 0) {
 #pragma unroll
             for (int j = 0; j < kGroup; ++j)
@@ -353,23 +381,25 @@ __global__ __launch_bounds__(256) void k_dispatch(DispatchArgs a)
                 }
         }
         if constexpr (OUT != 0) {
-            for (int v = v0 + tid; v < v1; v += bd) {
-                const u32x4 x = v == v0 + tid ? x0 : ld_row<DT, TAIL>(xrow, v, hidden);
-                if constexpr (OUT == 1) {
+            auto emit = [&](int v, u32x4 xv) {
+                uint32_t q[2];
+                if constexpr (OUT == 2)
+                    i8_codes<DT>(xv, inv, q);
 #pragma unroll
-                    for (int j = 0; j < kGroup; ++j)
-                        if (key[j] < a.experts)
-                            st_row<DT, TAIL>(static_cast<char*>(a.rows) + (size_t)c[j] * a.ld_rows * Elem<DT>::kBytes,
-                                             v, hidden, x);
-                } else {
-                    uint32_t q[2];
-                    i8_codes<DT>(x, inv, q);
-#pragma unroll
-                    for (int j = 0; j < kGroup; ++j)
-                        if (key[j] < a.experts)
+                for (int j = 0; j < kGroup; ++j)
+                    if (key[j] < a.experts) {
+                        if constexpr (OUT == 1)
+                            st_row<DT, TAIL>(static_cast<char*>(a.rows) + (size_t)c[j] * a.ld_rows * Elem<DT>::kBytes, v, hidden, xv);
+                        else
                             st_codes<DT, TAIL>(static_cast<char*>(a.rows) + (size_t)c[j] * a.ld_rows, v, hidden, q);
-                }
-            }
+                    }
+            };
+#pragma unroll
+            for (int u = 0; u < XN; ++u)
+                if (v0 + tid + u * bd < v1)
+                    emit(v0 + tid + u * bd, fixed<DT, TAIL>(x[u], v0 + tid + u * bd, hidden));
+            for (int v = v0 + tid + XN * bd; v < v1; v += bd)
+                emit(v, ld_row<DT, TAIL>(xrow, v, hidden));
             if constexpr (OUT == 2) {
                 if (blockIdx.y == 0)
 #pragma unroll

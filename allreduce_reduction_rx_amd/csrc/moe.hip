@@ -28,32 +28,28 @@ __device__ __forceinline__ int local_expert(int id, int first, int experts)
     return e < (uint32_t)experts ? (int)e : experts;     // `experts`: dropped
 }
 
-// Sums of c[0 .. N) over the workgroup, in every thread.
+// Sums of c[0 .. N) over the workgroup: sum j in lane j of every wave.
 template <int N>
-__device__ __forceinline__ void block_counts(uint32_t* c, uint32_t* lds)
+__device__ __forceinline__ uint32_t block_counts(const uint32_t* c, uint32_t* lds)
 {
     const int lane = lane_id(), wave = threadIdx.x / kWave, nw = blockDim.x / kWave;
+    uint32_t mine = 0;
 #pragma unroll
-    for (int j = 0; j < N; ++j)
-        c[j] = wave_sum_u(c[j]);
+    for (int j = 0; j < N; ++j) {
+        const uint32_t sum = wave_sum_u(c[j]);
+        mine = lane == j ? sum : mine;
+    }
     if (nw == 1)
-        return;
+        return mine;
     __syncthreads();   // the previous use of lds is over
-    if (lane == 0)
-#pragma unroll
-        for (int j = 0; j < N; ++j)
-            lds[wave * N + j] = c[j];
+    if (lane < N)
+        lds[wave * N + lane] = mine;
     __syncthreads();
-#pragma unroll
-    for (int j = 0; j < N; ++j)
-        c[j] = 0;
-    for (int w = 0; w < nw; ++w)
-#pragma unroll
-        for (int j = 0; j < N; ++j)
-            c[j] += lds[w * N + j];
-#pragma unroll
-    for (int j = 0; j < N; ++j)
-        c[j] = (uint32_t)__builtin_amdgcn_readfirstlane((int)c[j]);
+    mine = 0;
+    if (lane < N)
+        for (int w = 0; w < nw; ++w)
+            mine += lds[w * N + lane];
+    return mine;
 }
 
 // Segment s, expert e: pairs of the segment that go to e, in
@@ -303,7 +299,7 @@ __global__ __launch_bounds__(256) void k_dispatch(DispatchArgs a)
 {
     __shared__ uint32_t lds[4 * (kGroup + 1)];
     __shared__ uint32_t tops[4];
-    const int tid = threadIdx.x, bd = blockDim.x;
+    const int tid = threadIdx.x, bd = blockDim.x, lane = lane_id();
     const uint32_t t = blockIdx.x;
 
     if (t >= a.tokens) {
@@ -316,11 +312,9 @@ __global__ __launch_bounds__(256) void k_dispatch(DispatchArgs a)
         for (int j = 0; j < kGroup; ++j)
             to[j] = pair_key(e0 + j < a.experts ? e0 + j : a.experts, 0);
         count_below<kGroup>(a, to, c);
-        block_counts<kGroup>(c, lds);
-#pragma unroll
-        for (int j = 0; j < kGroup; ++j)
-            if (tid == j && e0 + j <= a.experts)
-                a.offsets[e0 + j] = (int)c[j];
+        const uint32_t n = block_counts<kGroup>(c, lds);
+        if (tid < kGroup && e0 + tid <= a.experts)
+            a.offsets[e0 + tid] = (int)n;
         return;
     }
 
@@ -341,13 +335,13 @@ __global__ __launch_bounds__(256) void k_dispatch(DispatchArgs a)
     for (int j0 = 0; j0 < a.topk; j0 += kGroup) {
         const int nj = a.topk - j0 < kGroup ? a.topk - j0 : kGroup;
         const uint32_t i0 = t * (uint32_t)a.topk + (uint32_t)j0;
-        int key[kGroup];
+        // lane j of every wave: pair i0 + j
+        const int key = lane < nj ? local_expert(a.ids[i0 + lane], a.first, a.experts) : a.experts;
+        const bool here = key < a.experts;
         uint32_t c[kGroup + 1], to[kGroup + 1];
 #pragma unroll
-        for (int j = 0; j < kGroup; ++j) {
-            key[j] = j < nj ? local_expert(a.ids[i0 + j], a.first, a.experts) : a.experts;
-            to[j] = pair_key(key[j], i0 + j);
-        }
+        for (int j = 0; j < kGroup; ++j)
+            to[j] = (uint32_t)__builtin_amdgcn_readlane((int)pair_key(key, i0 + lane), j);
         to[kGroup] = pair_key(a.experts, 0);   // all that are kept
         count_below<kGroup + 1>(a, to, c);
         if (OUT == 2 && j0 == 0) {
@@ -362,37 +356,35 @@ __global__ __launch_bounds__(256) void k_dispatch(DispatchArgs a)
             if (lane_id() == 0)
                 tops[tid / kWave] = m;
         }
-        block_counts<kGroup + 1>(c, lds);   // with several waves: barriers after tops is written
-        kept = c[kGroup];
+        const uint32_t place = block_counts<kGroup + 1>(c, lds);   // with several waves: barriers after tops is written
+        kept = (uint32_t)__builtin_amdgcn_readlane((int)place, kGroup);
         if (OUT == 2 && j0 == 0) {
             uint32_t m = tops[0];
             for (int w = 1; w < bd / kWave; ++w)
                 m = umax(m, tops[w]);
             i8_scale(bits_f32(m), scale, inv);
         }
-        if (blockIdx.y == 0) {
-#pragma unroll
-            for (int j = 0; j < kGroup; ++j)
-                if (tid == j && j < nj) {
-                    const bool here = key[j] < a.experts;
-                    a.slots[i0 + j] = here ? (int)c[j] : -1;
-                    if (here)
-                        a.order[c[j]] = (int)(i0 + j);
-                }
+        if (tid < nj && blockIdx.y == 0) {
+            a.slots[i0 + tid] = here ? (int)place : -1;
+            if (here) {
+                a.order[place] = (int)(i0 + tid);
+                if constexpr (OUT == 2)
+                    a.row_scales[place] = scale;
+            }
         }
         if constexpr (OUT != 0) {
+            const uint64_t mask = __ballot(here);
             auto emit = [&](int v, u32x4 xv) {
                 uint32_t q[2];
                 if constexpr (OUT == 2)
                     i8_codes<DT>(xv, inv, q);
-#pragma unroll
-                for (int j = 0; j < kGroup; ++j)
-                    if (key[j] < a.experts) {
-                        if constexpr (OUT == 1)
-                            st_row<DT, TAIL>(static_cast<char*>(a.rows) + (size_t)c[j] * a.ld_rows * Elem<DT>::kBytes, v, hidden, xv);
-                        else
-                            st_codes<DT, TAIL>(static_cast<char*>(a.rows) + (size_t)c[j] * a.ld_rows, v, hidden, q);
-                    }
+                for (uint64_t left = mask; left; left &= left - 1) {
+                    const size_t p = (uint32_t)__builtin_amdgcn_readlane((int)place, __builtin_ctzll(left));
+                    if constexpr (OUT == 1)
+                        st_row<DT, TAIL>(static_cast<char*>(a.rows) + p * a.ld_rows * Elem<DT>::kBytes, v, hidden, xv);
+                    else
+                        st_codes<DT, TAIL>(static_cast<char*>(a.rows) + p * a.ld_rows, v, hidden, q);
+                }
             };
 #pragma unroll
             for (int u = 0; u < XN; ++u)
@@ -400,13 +392,6 @@ __global__ __launch_bounds__(256) void k_dispatch(DispatchArgs a)
                     emit(v0 + tid + u * bd, fixed<DT, TAIL>(x[u], v0 + tid + u * bd, hidden));
             for (int v = v0 + tid + XN * bd; v < v1; v += bd)
                 emit(v, ld_row<DT, TAIL>(xrow, v, hidden));
-            if constexpr (OUT == 2) {
-                if (blockIdx.y == 0)
-#pragma unroll
-                    for (int j = 0; j < kGroup; ++j)
-                        if (tid == j && key[j] < a.experts)
-                            a.row_scales[c[j]] = scale;
-            }
         }
     }
 

@@ -9,25 +9,43 @@
 namespace rx {
 namespace {
 
-// y = the sources' sum, B sources' loads of a thread in flight together.
+// y = the sources' sum in their order, B sources' loads of a thread in flight
+// together.
 template <int DT, bool TAIL, int NV>
 __device__ __forceinline__ void fold_row(const void* const* src, int nsrc, size_t row_bytes, int hidden,
                                          float (*y)[Elem<DT>::kVE])
 {
-    constexpr int B = NV == 1 ? 8 : 4;   // more would cost a longer row its occupancy
+    constexpr int VE = Elem<DT>::kVE, B = NV == 1 ? 8 : 4;   // more would cost a longer row its occupancy
     const int tid = (int)threadIdx.x, bd = (int)blockDim.x;
-    int r;
-    switch (nsrc < B ? nsrc : B) {
-    case 1: fold_batch<DT, TAIL, NV, 1, true>(src, 0, row_bytes, hidden, tid, bd, y); return;
-    case 2: fold_batch<DT, TAIL, NV, 2, true>(src, 0, row_bytes, hidden, tid, bd, y); return;
-    case 3: fold_batch<DT, TAIL, NV, 3, true>(src, 0, row_bytes, hidden, tid, bd, y); return;
-    case 8: fold_batch<DT, TAIL, NV, B, true>(src, 0, row_bytes, hidden, tid, bd, y); r = B; break;
-    default: fold_batch<DT, TAIL, NV, 4, true>(src, 0, row_bytes, hidden, tid, bd, y); r = 4;
-    }
-    for (; r + 4 <= nsrc; r += 4)
-        fold_batch<DT, TAIL, NV, 4, false>(src, r, row_bytes, hidden, tid, bd, y);
-    for (; r < nsrc; ++r)
-        fold_batch<DT, TAIL, NV, 1, false>(src, r, row_bytes, hidden, tid, bd, y);
+#pragma unroll
+    for (int u = 0; u < NV; ++u)
+#pragma unroll
+        for (int k = 0; k < VE; ++k)
+            y[u][k] = -0.0f;   // x + -0 = x for every x
+    auto batch = [&](int r) {
+        u32x4 x[B][NV];
+#pragma unroll
+        for (int b = 0; b < B; ++b)
+            if (r + b < nsrc)
+#pragma unroll
+                for (int u = 0; u < NV; ++u)
+                    x[b][u] = ld_raw<DT, TAIL, true>(static_cast<const char*>(src[r + b]) + row_bytes, tid + u * bd, hidden);
+#pragma unroll
+        for (int b = 0; b < B; ++b)
+            if (r + b < nsrc)
+#pragma unroll
+                for (int u = 0; u < NV; ++u) {
+                    float f[VE];
+                    unpack<DT>(fixed<DT, TAIL>(x[b][u], tid + u * bd, hidden), f);
+#pragma unroll
+                    for (int k = 0; k < VE; ++k)
+                        y[u][k] += f[k];
+                }
+    };
+    batch(0);   // its pointers come with the kernel's arguments
+#pragma unroll 1
+    for (int r = B; r < nsrc; r += B)
+        batch(r);
 }
 
 // NV 1: the gate and the weights are loaded before the sources too, so that a

@@ -15,8 +15,8 @@
 //
 // The next row's loads go out as soon as this row's are unpacked, before the
 // sums, the results and the stores of this row: 80 KiB in flight a CU. HBM
-// bound: 16384 x 8192 BF16 over two sources takes 355 us for 1.88 GB read and
-// written (5.3 TB/s; a large copy reaches 5.1).
+// bound: 16384 x 8192 BF16 over two sources takes 366 us for 1.88 GB read and
+// written (5.1 TB/s, what a large copy reaches).
 //
 // MULTI: the part may see several gate rows. A gate row whose rows all lie in
 // the part is written at once; one that crosses the part's start goes to
@@ -210,15 +210,31 @@ __global__ __launch_bounds__(WG, WG > 512 ? 4 : 2) void k_norm_backward(NormBwdA
     const size_t r1 = r0 + a.part_rows < a.rows ? r0 + a.part_rows : a.rows;
 
     float acc_t[E] = {}, acc_pre[E] = {};
-    u32x4 wpost[NV], wpre[NV], gv[NV];
+    // where registers are short the weights and the gate wait in LDS (4096 x
+    // 5120 FP32 with a gate for each 100 rows, both directions: 266 -> 206 us)
+    constexpr bool kWeightsInLds = !ACC && (NV == 3 || (MULTI && NV == 2 && DT == 1));
+    __shared__ u32x4 wlds[kWeightsInLds ? 3 : 1][kWeightsInLds ? NV : 1][kWeightsInLds ? WG : 1];
+    u32x4 wreg[3][NV];
+    auto keep = [&](int which, int u, u32x4 x) {   // 0: w_post, 1: w_pre, 2: the gate
+        if constexpr (kWeightsInLds)
+            wlds[which][u][threadIdx.x] = x;
+        else
+            wreg[which][u] = x;
+    };
+    auto kept = [&](int which, int u) {
+        if constexpr (kWeightsInLds)
+            return wlds[which][u][threadIdx.x];
+        else
+            return held(wreg[which][u]);
+    };
     u32x4* lt = reinterpret_cast<u32x4*>(dyn) + tid;
     u32x4* lp = lt + (size_t)W * (E / 4);
 #pragma unroll
     for (int u = 0; u < NV; ++u) {
         const int v = tid + u * W;
-        wpost[u] = a.w_post ? ld_row<DT, TAIL>(a.w_post, v, hidden) : ones(DT);
-        wpre[u] = a.w_pre ? ld_row<DT, TAIL>(a.w_pre, v, hidden) : ones(DT);
-        gv[u] = ones(DT);
+        keep(0, u, a.w_post ? ld_row<DT, TAIL>(a.w_post, v, hidden) : ones(DT));
+        keep(1, u, a.w_pre ? ld_row<DT, TAIL>(a.w_pre, v, hidden) : ones(DT));
+        keep(2, u, ones(DT));
     }
     if constexpr (ACC)
 #pragma unroll
@@ -258,7 +274,7 @@ __global__ __launch_bounds__(WG, WG > 512 ? 4 : 2) void k_norm_backward(NormBwdA
         if (a.gate)
 #pragma unroll
             for (int u = 0; u < NV; ++u)
-                gv[u] = ld_row<DT, TAIL>(static_cast<const char*>(a.gate) + grp * a.hidden * EB, tid + u * W, hidden);
+                keep(2, u, ld_row<DT, TAIL>(static_cast<const char*>(a.gate) + grp * a.hidden * EB, tid + u * W, hidden));
         for (size_t t = s0 + team; t < s1; t += R) {
             if (!kRun && have != t)
                 load(t);
@@ -286,7 +302,7 @@ __global__ __launch_bounds__(WG, WG > 512 ? 4 : 2) void k_norm_backward(NormBwdA
             for (int u = 0; u < NV; ++u) {
                 float pre[VE];
                 auto whole = [&](u32x4 x) { return fixed<DT, TAIL>(x, tid + u * W, hidden); };
-                row_sums<DT, VE>(y[u], whole(res[u]), whole(dhv[u]), whole(dzv[u]), held(wpost[u]), held(wpre[u]), held(gv[u]), p, q,
+                row_sums<DT, VE>(y[u], whole(res[u]), whole(dhv[u]), whole(dzv[u]), kept(0, u), kept(1, u), kept(2, u), p, q,
                                  a.residual_scale, h[u], e[u], pre, s);
                 add_to<ACC, VE>(acc_pre + u * VE, lp + u * (VE / 4) * W, W, pre);
             }
@@ -301,7 +317,7 @@ __global__ __launch_bounds__(WG, WG > 512 ? 4 : 2) void k_norm_backward(NormBwdA
 #pragma unroll
             for (int u = 0; u < NV; ++u) {
                 float o1[VE], o2[VE], tt[VE];
-                row_results<DT, VE>(y[u], h[u], e[u], held(wpost[u]), held(gv[u]), p, m1, m2, a.residual_scale, o1, o2, tt);
+                row_results<DT, VE>(y[u], h[u], e[u], kept(0, u), kept(2, u), p, m1, m2, a.residual_scale, o1, o2, tt);
                 add_to<ACC, VE>(acc_t + u * VE, lt + u * (VE / 4) * W, W, tt);
                 const int v = tid + u * W;
                 if (a.d_residual)
@@ -316,8 +332,8 @@ __global__ __launch_bounds__(WG, WG > 512 ? 4 : 2) void k_norm_backward(NormBwdA
 #pragma unroll
             for (int u = 0; u < NV; ++u) {
                 float w1[VE], g[VE], tv[VE];
-                unpack<DT>(held(wpost[u]), w1);
-                unpack<DT>(held(gv[u]), g);
+                unpack<DT>(kept(0, u), w1);
+                unpack<DT>(kept(2, u), g);
                 take<ACC, VE>(acc_t + u * VE, lt + u * (VE / 4) * W, W, tv);
                 join_teams<R, W, VE>(tv, team, tid, dyn);
                 const uint32_t c = (uint32_t)((tid + u * W) * VE);

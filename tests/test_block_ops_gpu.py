@@ -144,7 +144,8 @@ def test_dispatch_rows(dtype, strided, tokens, topk, hidden, drop):
 @pytest.mark.parametrize("dtype", DTYPES)
 @pytest.mark.parametrize("int8", [False, True])
 @pytest.mark.parametrize("tokens,topk,hidden,experts,total", [
-    (4099, 1, 65, 3, 4), (1025, 8, 1000, 100, 256), (70, 60, 2500, 200, 300), (3000, 5, 264, 1024, 1500)])
+    (4099, 1, 65, 3, 4), (1025, 8, 1000, 100, 256), (70, 60, 2500, 200, 300), (3000, 5, 264, 1024, 1500),
+    (4097, 8, 40, 300, 400), (33000, 1, 24, 1000, 1000), (5461, 6, 24, 77, 90)])
 def test_dispatch_rows_of_many_pairs(dtype, int8, tokens, topk, hidden, experts, total):
     g = gen(tokens)
     ids = routing(g, tokens, topk, total, 0.05)

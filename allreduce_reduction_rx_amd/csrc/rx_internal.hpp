@@ -78,8 +78,8 @@ struct DispatchArgs {
     int topk, first, experts;
 };
 
-// Up to this many pairs every token's workgroup counts over all of them in
-// the one launch; above, segments are counted first (moe.hip).
+// The most pairs that one launch counts for every token, and that need no
+// workspace (moe.hip).
 constexpr size_t kDispatchCountAll = 4096;
 
 struct CombineArgs {

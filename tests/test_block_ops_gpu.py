@@ -266,7 +266,10 @@ def norm_case(g, rows, hidden, nsrc, dtype, post, gate_rows, residual=True):
 NORMS = [  # rows, hidden, sources, norm after the block, rows of a gate row (0: no gate)
     (1, 1, 1, True, 1), (1, 8192, 8, True, 1), (5, 7, 2, True, 2), (32, 264, 3, False, 0), (9, 1001, 16, True, 4),
     (300, 96, 5, True, 300), (1030, 72, 2, True, 700), (600, 40, 1, False, 3), (700, 130, 4, True, 1),
-    (4, 5001, 6, True, 3), (3, 16384, 2, True, 2), (2, 32768, 1, True, 0), (3, 20003, 7, False, 1)]
+    (4, 5001, 6, True, 3), (3, 16384, 2, True, 2), (2, 32768, 1, True, 0), (3, 20003, 7, False, 1),
+    # more rows than workgroups at each width that has a kernel of its own
+    (530, 5203, 3, True, 130), (300, 9001, 2, True, 70), (300, 7000, 5, True, 0), (290, 12300, 1, False, 3), (259, 17000, 2, True, 100),
+    (2100, 500, 9, True, 8), (2100, 1020, 2, True, 5), (3000, 64, 2, False, 1100)]
 
 
 @pytest.mark.parametrize("dtype", DTYPES)

@@ -21,11 +21,12 @@
 // MULTI: the part may see several gate rows. A gate row whose rows all lie in
 // the part is written at once; one that crosses the part's start goes to
 // slot 0 of the part's two, one that only crosses its end to slot 1.
-// ACC: rows of 1025 to 2048 vectors, where 1024 threads leave 128 registers
-// a thread: the parameters' sums stay in LDS and nothing is loaded ahead
-// (4096 x 16384 BF16, forward and backward: 432 us, against 717 us with four
-// vectors a thread loaded ahead and 807 us with k_norm_backward_long, which
-// takes the rows above).
+// ACC: the parameters' sums stay in LDS instead of registers: rows of 1025 to
+// 1536 vectors in BF16 (three vectors a thread; 4096 x 10240, forward and
+// backward: 296 us, 344 with 1024 threads), and all rows of 1537 to 2048, where
+// 1024 threads leave 128 registers a thread and nothing is loaded ahead (4096 x
+// 16384 BF16: 432 us, against 717 us with four vectors a thread loaded ahead and
+// 807 us with k_norm_backward_long, which takes the rows above).
 #include "norm_common.hpp"
 
 namespace rx {

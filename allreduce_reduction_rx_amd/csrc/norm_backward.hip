@@ -177,11 +177,14 @@ __device__ __forceinline__ void row_results(const float* y, const float* h, cons
     }
 }
 
-// The two means, from the three sums.
+// The two means, from the three sums, multiplied outwards from the sum: S1 / H
+// is at most rms(a) / q, so every step lies between it and the result. q^3
+// by itself would leave FP32's range for rows of 1e13 or more, and be infinite
+// for a row of zeros with eps below 2e-26, whose mean is 0.
 __device__ __forceinline__ void row_means(const NormBwdArgs& a, const float* s, float p, float q, float& m1, float& m2)
 {
-    m1 = q * q * q * (s[0] * a.inv_hidden);
-    m2 = a.w_post ? p * p * ((s[1] - m1 * s[2]) * a.inv_hidden) : 0.0f;
+    m1 = s[0] * a.inv_hidden * q * q * q;
+    m2 = a.w_post ? (s[1] - m1 * s[2]) * a.inv_hidden * p * p : 0.0f;
 }
 
 // Where the sum of gate row grp goes from this part.

@@ -1,0 +1,50 @@
+"""The operators around a block's allreduce at the edges of what their calls
+accept, against their float64 forms (block_ref.py)."""
+import pytest
+import torch
+
+import allreduce_reduction_rx_amd as rx
+import block_ref as R
+from test_block_ops_gpu import BF16, DTYPES, FP32, Strided, gen, gpu, norm_case, put, randn, within
+
+pytestmark = pytest.mark.gpu
+
+
+# ---- norm: rows of any size ------------------------------------------------------
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("post", [True, False])
+@pytest.mark.parametrize("hidden", [136, 16400, 20000])   # registers, 1024 threads or long rows, long rows
+@pytest.mark.parametrize("scale,eps", [(1e16, 1e-5), (1e14, 1e-5), (1e-13, 1e-30), (1e-15, 1e-30), (1.0, 1e-30)])
+def test_norm_gradient_of_rows_far_from_one(scale, eps, hidden, post, dtype):
+    """Rows whose size, cubed, is no float32, and rows of zeros whose statistic is 1 / sqrt(eps). The bounds
+    count relative roundings; every value on the way is a normal float32."""
+    g = gen(hidden)
+    rows, rs, eps = 9, 0.75, torch.tensor(eps).item()   # eps: the float32 that the call gets
+    t, groups = norm_case(g, rows, hidden, 2, dtype, post, 4)
+    t["srcs"] = [(s.double() * scale).to(dtype) for s in t["srcs"]]
+    t["residual"] = (t["residual"].double() * scale).to(dtype)
+    for s in (*t["srcs"], t["residual"]):
+        s[5] = 0
+    f = R.norm(t["srcs"], t["residual"], t["gate"], 4, t["w_post"], t["w_pre"], rs, eps)
+    srcs, res, gate, wp, wz = [gpu(s) for s in t["srcs"]], *(gpu(t[k]) for k in ("residual", "gate", "w_post", "w_pre"))
+    new = lambda *s, dtype=FP32: torch.full(s, 77.0, dtype=dtype, device="cuda")
+    h, z, d_src, d_res = (new(rows, hidden, dtype=dtype) for _ in range(4))
+    p, q = new(rows), new(rows)
+    rx.rx_residual_norm(srcs, res, gate, wp, wz, h, z, rstd_post=p if post else None, rstd_pre=q, gate_rows=4,
+                        residual_scale=rs, eps=eps)
+    n = f["n"] * R.EPS32 * f["kappa"]
+    within(h, f["h"], R.cast_bound(f["h"], n * f["hm"], dtype))
+    within(z, f["z"], R.cast_bound(f["z"], n * f["zm"], dtype))
+    within(q, f["q"][:, 0], (n * f["q"])[:, 0])
+
+    d_z = randn(g, rows, hidden, dtype=dtype)
+    d_gate, d_wp, d_wz = new(groups, hidden), new(hidden) if post else None, new(hidden)
+    ws = torch.full((rx.rx_residual_norm_backward_workspace(rows, hidden, 4),), 0xFF, dtype=torch.uint8, device="cuda")
+    rx.rx_residual_norm_backward(srcs, res, gate, wp, wz, p if post else None, q, None, gpu(d_z), d_src, d_res,
+                                 d_gate=d_gate, d_w_post=d_wp, d_w_pre=d_wz, gate_rows=4, residual_scale=rs, workspace=ws)
+    want = R.norm_backward(f, None, d_z, rs, post, groups)
+    for name, got in (("d_src", d_src), ("d_residual", d_res), ("d_gate", d_gate), ("d_w_post", d_wp), ("d_w_pre", d_wz)):
+        if got is not None:
+            value, err = want[name]
+            within(got, value, R.cast_bound(value, err, got.dtype))

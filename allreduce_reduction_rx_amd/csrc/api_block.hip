@@ -137,9 +137,10 @@ rx_status_t rx_moe_combine_backward(const void* d_out, size_t ld_d_out, const vo
                                     size_t tokens, int topk, size_t hidden, rx_dtype_t dtype, void* d_rows,
                                     size_t ld_d_rows, float* d_weights, hipStream_t stream)
 {
-    if (tokens > 0 && (!slots || !kept))
+    const bool clears = nrows > 0 && hidden > 0;   // rows that no pair owns, also without tokens
+    if ((tokens > 0 && (!slots || !kept)) || (clears && (!kept || !d_rows)))
         return RX_ERR_NULL;
-    if (tokens > 0 && hidden > 0 && (!d_out || (nrows > 0 && (!d_rows || (d_weights && !rows)))))
+    if (tokens > 0 && hidden > 0 && (!d_out || (nrows > 0 && d_weights && !rows)))
         return RX_ERR_NULL;
     if (topk < 1 || topk > kMaxTopk || tokens > kMaxRows || nrows >= ((size_t)1 << 31) || hidden > kMaxHidden ||
         bad_ld(ld_d_out, hidden, tokens) || bad_ld(ld_d_rows, hidden, nrows) ||
@@ -150,7 +151,9 @@ rx_status_t rx_moe_combine_backward(const void* d_out, size_t ld_d_out, const vo
     if (!element_aligned(d_out, dtype) || !element_aligned(rows, dtype) || !element_aligned(d_rows, dtype) ||
         !aligned4(slots) || !aligned4(weights) || !aligned4(kept) || !aligned4(d_weights))
         return RX_ERR_ALIGN;
-    if (tokens == 0)
+    // without a device there is no memory that the rows could lie in: a call without tokens succeeds there
+    int device;
+    if (tokens == 0 && (!clears || hipGetDevice(&device) != hipSuccess))
         return RX_OK;
     CombineBwdArgs a = {};
     a.d_out = d_out;

@@ -523,8 +523,9 @@ __global__ __launch_bounds__(256) void k_combine_backward(CombineBwdArgs a)
     const int hidden = (int)a.hidden;
     const int nvec = (hidden + VE - 1) / VE;
     const void* grow = static_cast<const char*>(a.d_out) + t * a.ld_d_out * Elem<DT>::kBytes;
-    for (int j0 = 0; j0 < a.topk; j0 += kGroup) {
-        const int nj = a.topk - j0 < kGroup ? a.topk - j0 : kGroup;
+    const int topk = t < a.tokens ? a.topk : 0;   // a call without tokens has workgroups for the rows' zeros
+    for (int j0 = 0; j0 < topk; j0 += kGroup) {
+        const int nj = topk - j0 < kGroup ? topk - j0 : kGroup;
         float dot[kGroup] = {};
         for (int base = tid; base < nvec; base += bd * NV) {
             float g[NV][VE];
@@ -583,7 +584,7 @@ __global__ __launch_bounds__(256) void k_combine_backward(CombineBwdArgs a)
     }
     const u32x4 zero = {0, 0, 0, 0};
     const int kept = *a.kept < 0 ? 0 : *a.kept;
-    for (size_t p = (size_t)kept + t; p < a.nrows; p += a.tokens)
+    for (size_t p = (size_t)kept + t; p < a.nrows; p += gridDim.x)
         for (int v = tid; v < nvec; v += bd)
             st_row<DT, TAIL, true>(static_cast<char*>(a.d_rows) + p * a.ld_d_rows * Elem<DT>::kBytes, v, hidden, zero);
 }
@@ -707,7 +708,8 @@ hipError_t launch_combine_backward(const CombineBwdArgs& in, int dtype, hipStrea
         fn = two ? backward_fn<2, true>(dtype, tail) : backward_fn<1, true>(dtype, tail);
     else
         fn = two ? backward_fn<2, false>(dtype, tail) : backward_fn<1, false>(dtype, tail);
-    return launch_logged("k_combine_backward", fn, dim3((unsigned)a.tokens), dim3(wg), params, s);
+    const size_t clearing = (size_t)device_cu_count() * 8 < a.nrows ? (size_t)device_cu_count() * 8 : a.nrows;
+    return launch_logged("k_combine_backward", fn, dim3((unsigned)(a.tokens ? a.tokens : clearing)), dim3(wg), params, s);
 }
 
 }  // namespace rx

@@ -382,7 +382,7 @@ rx_status_t rx_moe_combine(const void* rows, size_t ld_rows, size_t nrows,
  * Gradient of rx_moe_combine, for slots that rx_moe_dispatch wrote (each row
  * is owned by at most one pair, kept rows are 0 .. *kept - 1):
  *   d_rows[slots[t, j], :] = cast( weights[t, j] d_out[t, :] ), 0 for the
- *                            rows from *kept to nrows
+ *                            rows from *kept to nrows, also with tokens == 0
  *   d_weights[t, j]        = sum over c of d_out[t, c] rows[slots[t, j], c]
  *                            in FP32, 0 for a dropped pair
  * kept      : device pointer to the number of kept rows (offsets + experts).

@@ -48,3 +48,21 @@ def test_norm_gradient_of_rows_far_from_one(scale, eps, hidden, post, dtype):
         if got is not None:
             value, err = want[name]
             within(got, value, R.cast_bound(value, err, got.dtype))
+
+
+# ---- combine: no tokens ------------------------------------------------------------
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("hidden", [1, 7, 264, 4100])
+@pytest.mark.parametrize("nrows,kept", [(1, 0), (5, 0), (5, 3), (5, 5), (3000, 0), (3000, 2999), (4, 9), (0, 0)])
+def test_combine_gradient_without_tokens(nrows, kept, hidden, dtype):
+    """A rank whose tokens went elsewhere, with a row buffer of its own size: rows from kept on are 0."""
+    i32 = dict(dtype=torch.int32, device="cuda")
+    d_rows = Strided(nrows, hidden, dtype)
+    offsets = torch.tensor([0, kept], **i32)
+    empty = torch.empty(0, hidden, dtype=dtype, device="cuda")
+    for rows, d_w in ((None, None), (torch.ones(nrows, hidden, dtype=dtype, device="cuda"), torch.empty(0, 2, device="cuda"))):
+        d_rows.full.fill_(77.0)
+        rx.rx_moe_combine_backward(empty, rows, torch.empty(0, 2, **i32), None, offsets, d_rows.t, d_w)
+        assert bool((d_rows.t[kept:] == 0).all()) and bool((d_rows.t[:kept] == 77).all())
+        d_rows.check()

@@ -353,7 +353,7 @@ __global__ __launch_bounds__(256) void k_dispatch(DispatchArgs a)
             x[u] = ld_raw<DT, TAIL>(xrow, v0 + tid + u * bd, hidden);
 
     float scale = 1.0f, inv = 1.0f;
-    uint32_t kept = 0;
+    uint32_t kept = 0, top = 0;
     for (int j0 = 0; j0 < a.topk; j0 += kGroup) {
         const int nj = a.topk - j0 < kGroup ? a.topk - j0 : kGroup;
         const uint32_t i0 = t * (uint32_t)a.topk + (uint32_t)j0;
@@ -374,17 +374,17 @@ __global__ __launch_bounds__(256) void k_dispatch(DispatchArgs a)
             for (int v = tid; v < nvec; v += bd)   // the rest, and the other parts of a split row
                 if (v < v0 || v >= v0 + XN * bd)
                     m = umax(m, vec_absmax<DT>(ld_row<DT, TAIL>(xrow, v, hidden)));
-            m = group_max<kWave>(m);
-            if (lane_id() == 0)
-                tops[tid / kWave] = m;
+            top = group_max<kWave>(m);
+            if (bd > kWave && lane == 0)
+                tops[tid / kWave] = top;
         }
         const uint32_t place = block_counts<kGroup + 1>(c, lds);   // with several waves: barriers after tops is written
         kept = (uint32_t)__builtin_amdgcn_readlane((int)place, kGroup);
         if (OUT == 2 && j0 == 0) {
-            uint32_t m = tops[0];
-            for (int w = 1; w < bd / kWave; ++w)
-                m = umax(m, tops[w]);
-            i8_scale(bits_f32(m), scale, inv);
+            if (bd > kWave)   // one wave has its row's largest already, and no barrier behind it
+                for (int w = 0; w < bd / kWave; ++w)
+                    top = umax(top, tops[w]);
+            i8_scale(bits_f32(top), scale, inv);
         }
         if (tid < nj && blockIdx.y == 0) {
             a.slots[i0 + tid] = here ? (int)place : -1;

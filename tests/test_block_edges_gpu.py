@@ -5,7 +5,7 @@ import torch
 
 import allreduce_reduction_rx_amd as rx
 import block_ref as R
-from test_block_ops_gpu import BF16, DTYPES, FP32, Strided, gen, gpu, norm_case, put, randn, within
+from test_block_ops_gpu import BF16, DTYPES, FP32, Strided, gen, gpu, norm_case, put, randn, routing, run_dispatch, within
 
 pytestmark = pytest.mark.gpu
 
@@ -66,3 +66,20 @@ def test_combine_gradient_without_tokens(nrows, kept, hidden, dtype):
         rx.rx_moe_combine_backward(empty, rows, torch.empty(0, 2, **i32), None, offsets, d_rows.t, d_w)
         assert bool((d_rows.t[kept:] == 0).all()) and bool((d_rows.t[:kept] == 77).all())
         d_rows.check()
+
+
+# ---- dispatch: a workgroup of one wave ------------------------------------------------
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("tokens,topk", [(1, 1), (7, 2), (8, 8), (1, 64), (4, 16), (13, 5)])   # 64 pairs and one more
+@pytest.mark.parametrize("hidden", [1, 250, 256, 257, 512, 513])                 # 64 vectors and one more
+def test_dispatch_int8_of_few_pairs_and_short_rows(tokens, topk, hidden, dtype):
+    """Rows whose largest value one wave finds alone, and those that several find together."""
+    g = gen(tokens + hidden)
+    ids = routing(g, tokens, topk, 64)
+    x = randn(g, tokens, hidden, dtype=dtype) * (1 + torch.arange(tokens))[:, None].to(dtype)
+    _, order, _, rows, scales = run_dispatch(ids, 50, 3, x, int8=True)
+    codes, s = R.quant_i8(x)
+    kept = order >= 0
+    assert torch.equal(rows, R.gather(codes, order, topk))
+    assert torch.equal(scales[kept], s[order[kept].long() // topk]) and bool((scales[~kept] == 1).all())

@@ -268,6 +268,7 @@ int moe_combine_backward(PyObject* const* a, Py_ssize_t n)
 // What both directions of the residual norm read: a = srcs, residual, gate,
 // gate_rows (None: all rows share one), w_post, w_pre.
 struct NormInputs {
+    at::Tensor held[RX_MAX_SRC];   // the sources, which a generator alone may have had, until the launch
     const void* src[RX_MAX_SRC];
     int nsrc;
     size_t ld_src = 0, ld_residual = 0, gate_rows;
@@ -283,10 +284,10 @@ NormInputs norm_inputs(int dev, PyObject* const* a)
     PyObject* seq = PySequence_Fast(a[0], "srcs must be a sequence of tensors");
     if (!seq)
         throw Raised();
-    struct Held {
+    struct Listed {
         PyObject* o;
-        ~Held() { Py_DECREF(o); }
-    } held{seq};
+        ~Listed() { Py_DECREF(o); }
+    } listed{seq};
     const Py_ssize_t n = PySequence_Fast_GET_SIZE(seq);
     if (n < 1 || n > RX_MAX_SRC)
         refuse(PyExc_ValueError, "1 to %d sources, not %d", RX_MAX_SRC, (int)n);
@@ -305,6 +306,7 @@ NormInputs norm_inputs(int dev, PyObject* const* a)
             in.ld_src = ld;
         else if (ld != in.ld_src)
             refuse(PyExc_ValueError, "srcs[%d] has another row stride than srcs[0]", (int)k);
+        in.held[k] = t;
         in.src[k] = t.data_ptr();
     }
     if (given(a[1])) {

@@ -83,3 +83,33 @@ def test_dispatch_int8_of_few_pairs_and_short_rows(tokens, topk, hidden, dtype):
     kept = order >= 0
     assert torch.equal(rows, R.gather(codes, order, topk))
     assert torch.equal(scales[kept], s[order[kept].long() // topk]) and bool((scales[~kept] == 1).all())
+
+
+# ---- the binding: who holds the sources ---------------------------------------------------
+
+def test_sources_of_a_generator_live_until_the_launch():
+    """The stream is looked up after the checks and before the launch: the tensors that only a generator had
+    must hold their memory then, and no longer after the call."""
+    import ctypes
+
+    g = gen(31)
+    data = [randn(g, 4, 96) for _ in range(3)]
+    h, want = torch.empty(4, 96, device="cuda"), torch.empty(4, 96, device="cuda")
+    rx.rx_residual_norm([t.cuda() for t in data], None, None, None, None, want, None)
+    L, m, held = rx.lib(), rx._bind(), []
+    at = [ctypes.cast(getattr(L, name), ctypes.c_void_p).value for name in (
+        "rx_moe_dispatch", "rx_moe_combine", "rx_moe_combine_backward", "rx_residual_norm", "rx_residual_norm_backward",
+        "rx_quant_i8", "rx_gemm_i8")]
+    before = torch.cuda.memory_allocated()
+
+    def stream(device):
+        held.append(torch.cuda.memory_allocated() - before)
+        return torch._C._cuda_getCurrentRawStream(device)
+
+    try:
+        m.connect(stream, *at)
+        rx.rx_residual_norm((t.cuda() for t in data), None, None, None, None, h, None)
+    finally:
+        m.connect(torch._C._cuda_getCurrentRawStream, *at)
+    assert len(held) == 1 and held[0] >= 3 * 4 * 96 * 4
+    assert torch.cuda.memory_allocated() == before and torch.equal(h, want)

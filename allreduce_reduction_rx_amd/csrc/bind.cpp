@@ -90,15 +90,19 @@ void check(int dev, at::ScalarType type, Sizes shape, const char* name, const at
 }
 
 // ... whose rows (its last dimension) are packed, at any stride: the stride.
+// The stride of a single row, or of rows without elements, may be any number
+// in a tensor: it is taken as the row's length.
 size_t block(int dev, at::ScalarType type, Sizes shape, const char* name, const at::Tensor& t)
 {
     check(dev, type, shape, name, t);
     const int64_t n = (int64_t)shape.size(), rows = t.size(n - 2), width = t.size(n - 1), ld = t.stride(n - 2);
-    if (width > 1 && t.stride(n - 1) != 1)
+    if (rows > 0 && width > 1 && t.stride(n - 1) != 1)
         refuse(PyExc_ValueError, "%s's rows must be contiguous", name);
-    if (rows > 1 && ld < width)
+    if (rows <= 1 || width == 0)
+        return (size_t)width;
+    if (ld < width)
         refuse(PyExc_ValueError, "%s's rows overlap", name);
-    return (size_t)(ld > width ? ld : width);
+    return (size_t)ld;
 }
 
 void* packed(int dev, at::ScalarType type, Sizes shape, const char* name, const at::Tensor& t)
@@ -386,6 +390,12 @@ int quant_i8(PyObject* const* a, Py_ssize_t n)
     return rx.quant_i8(x.data_ptr(), ld_x, rows, k, dt, codes.data_ptr(), ld_c, ps, stream);
 }
 
+// The product's row stride: of a row that has no second one, its whole chunks.
+size_t chunked(size_t ld, const at::Tensor& t, int64_t k)
+{
+    return t.size(-2) > 1 && k > 0 ? ld : (size_t)((k + 15) / 16 * 16);
+}
+
 // The product reads whole 16-byte chunks: the last row's must lie in the
 // tensor's storage too.
 void check_padded(const at::Tensor& t, int64_t k, const char* name)
@@ -410,19 +420,19 @@ int gemm_i8(PyObject* const* a, Py_ssize_t n)
     const int64_t rows = ta.size(0), k = ta.size(1), cols = tb.size(-2), experts = grouped ? tb.size(0) : 1;
     if (experts > INT32_MAX)
         refuse(PyExc_ValueError, "too many experts");
-    const size_t ld_a = block(w.dev, at::kChar, {rows, k}, "a", ta);
+    const size_t ld_a = chunked(block(w.dev, at::kChar, {rows, k}, "a", ta), ta, k);
     size_t ld_b, stride_b = 0;
     const int* offsets = nullptr;
     const float* sb;
     if (grouped) {
-        ld_b = block(w.dev, at::kChar, {experts, cols, k}, "b", tb);
+        ld_b = chunked(block(w.dev, at::kChar, {experts, cols, k}, "b", tb), tb, k);
         offsets = (const int*)packed(w.dev, at::kInt, {experts + 1}, "offsets", a[7]);
         if (tb.stride(0) < 0)
             refuse(PyExc_ValueError, "b's matrices must follow each other");
-        stride_b = (size_t)tb.stride(0);
+        stride_b = experts > 1 && tb.numel() > 0 ? (size_t)tb.stride(0) : 0;
         sb = (const float*)packed(w.dev, at::kFloat, {experts, cols}, "b_scales", tensor(a[5], "b_scales"));
     } else {
-        ld_b = block(w.dev, at::kChar, {cols, k}, "b", tb);
+        ld_b = chunked(block(w.dev, at::kChar, {cols, k}, "b", tb), tb, k);
         sb = (const float*)packed(w.dev, at::kFloat, {cols}, "b_scales", tensor(a[5], "b_scales"));
     }
     const float* sa = (const float*)packed(w.dev, at::kFloat, {rows}, "a_scales", tensor(a[3], "a_scales"));

@@ -113,3 +113,43 @@ def test_sources_of_a_generator_live_until_the_launch():
         m.connect(torch._C._cuda_getCurrentRawStream, *at)
     assert len(held) == 1 and held[0] >= 3 * 4 * 96 * 4
     assert torch.cuda.memory_allocated() == before and torch.equal(h, want)
+
+
+# ---- the binding: one row, no columns ----------------------------------------------------
+
+def test_one_row_has_no_stride():
+    """A single token's row, cut out of buffers of different widths."""
+    g = gen(21)
+    wide = [torch.zeros(1, 64 + 8 * j, dtype=BF16, device="cuda")[:, :64] for j in range(3)]
+    for t in wide:
+        t.copy_(randn(g, 1, 64, dtype=BF16))
+    far = torch.as_strided(wide[0], (1, 64), (1, 1))   # a row's own stride may be any number
+    h, want = torch.empty(1, 64, dtype=BF16, device="cuda"), torch.empty(1, 64, dtype=BF16, device="cuda")
+    rx.rx_residual_norm([far, *wide[1:]], None, None, None, None, h, None)
+    rx.rx_residual_norm([t.contiguous() for t in wide], None, None, None, None, want, None)
+    assert torch.equal(h, want)
+
+
+@pytest.mark.parametrize("grouped", [False, True])
+def test_gemm_of_one_row_and_one_channel(grouped):
+    g = gen(22)
+    a, b = (torch.randint(-127, 128, (112,), generator=g).to(torch.int8).cuda() for _ in range(2))
+    va, vb = a[:100].unsqueeze(0), b[:100].unsqueeze(0)   # strides of 100, rows padded to 112
+    one, out = torch.ones(1, device="cuda"), torch.empty(1, 1, device="cuda")
+    if grouped:
+        rx.rx_gemm_i8(va, one, vb.unsqueeze(0), one.view(1, 1), out, offsets=torch.tensor([0, 1], dtype=torch.int32, device="cuda"))
+    else:
+        rx.rx_gemm_i8(va, one, vb, one, out)
+    assert out.item() == (a[:100].double() @ b[:100].double()).item()
+
+
+@pytest.mark.parametrize("grouped", [False, True])
+def test_gemm_without_columns_gives_zeros(grouped):
+    i8 = dict(dtype=torch.int8, device="cuda")
+    out = torch.full((5, 3), 77.0, device="cuda")
+    if grouped:
+        rx.rx_gemm_i8(torch.empty(5, 0, **i8), torch.ones(5, device="cuda"), torch.empty(2, 3, 0, **i8), torch.ones(2, 3, device="cuda"), out,
+                      offsets=torch.tensor([0, 2, 4], dtype=torch.int32, device="cuda"))
+    else:
+        rx.rx_gemm_i8(torch.empty(5, 0, **i8), torch.ones(5, device="cuda"), torch.empty(3, 0, **i8), torch.ones(3, device="cuda"), out)
+    assert bool((out == 0).all())

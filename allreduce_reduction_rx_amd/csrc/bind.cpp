@@ -323,6 +323,11 @@ NormInputs norm_inputs(int dev, PyObject* const* a)
         refuse(PyExc_ValueError, "gate_rows must be positive");
     in.gate_rows = gate_rows < 1 ? 0 : (size_t)gate_rows;
     in.groups = gate_rows < 1 ? 0 : in.rows / gate_rows + (in.rows % gate_rows != 0);
+    // one gate row for all rows, of which there are none
+    if (in.rows == 0 && !given(a[3]) && given(a[2])) {
+        const at::Tensor& t = tensor(a[2], "gate");
+        in.groups = t.dim() > 0 && t.size(0) == 0 ? 0 : 1;
+    }
     in.gate = packed(dev, in.type, {in.groups, in.hidden}, "gate", a[2]);
     in.w_post = packed(dev, in.type, {in.hidden}, "w_post", a[4]);
     in.w_pre = packed(dev, in.type, {in.hidden}, "w_pre", a[5]);
@@ -370,6 +375,15 @@ int residual_norm_backward(PyObject* const* a, Py_ssize_t n)
     void* ws = workspace(w.dev, a[18], &bytes);
     const hipStream_t stream = w.stream();
     NoGil open;
+    // Without rows the C call knows no gate row, but writes a weight's gradient: zeros for the gate's, too.
+    if (in.rows == 0 && in.groups == 1 && dg) {
+        const int status = rx.residual_norm_backward(in.src, in.nsrc, 0, nullptr, 0, nullptr, 1, nullptr, nullptr, nullptr, nullptr,
+                                                     rs, 0, in.hidden, in.dtype, nullptr, 0, nullptr, 0, nullptr, in.hidden,
+                                                     nullptr, 0, nullptr, dg, nullptr, nullptr, 0, stream);
+        if (status != RX_OK)
+            return status;
+        dg = nullptr;
+    }
     return rx.residual_norm_backward(in.src, in.nsrc, in.ld_src, in.residual, in.ld_residual, in.gate, in.gate_rows, in.w_post,
                                      in.w_pre, p, q, rs, in.rows, in.hidden, in.dtype, dh, ld[0], dz, ld[1], ds,
                                      ld[2], dr, ld[3], dg, dwp, dwq, ws, bytes, stream);

@@ -153,3 +153,19 @@ def test_gemm_without_columns_gives_zeros(grouped):
     else:
         rx.rx_gemm_i8(torch.empty(5, 0, **i8), torch.ones(5, device="cuda"), torch.empty(3, 0, **i8), torch.ones(3, device="cuda"), out)
     assert bool((out == 0).all())
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("gate_len", [0, 1])
+def test_norm_without_rows_keeps_the_gate(gate_len, dtype):
+    """A gate for all rows is one row, also where there are none: its gradient is an empty sum."""
+    none = lambda: torch.empty(0, 72, dtype=dtype, device="cuda")
+    gate, w = torch.ones(gate_len, 72, dtype=dtype, device="cuda"), torch.ones(72, dtype=dtype, device="cuda")
+    stat = torch.empty(0, device="cuda")
+    rx.rx_residual_norm([none()], none(), gate, w, w, none(), none(), rstd_post=stat, rstd_pre=stat)
+    d = [torch.full(s, 77.0, device="cuda") for s in ((gate_len, 72), (72,), (72,))]
+    rx.rx_residual_norm_backward([none()], none(), gate, w, w, stat, stat, none(), none(), none(), none(), d_gate=d[0],
+                                 d_w_post=d[1], d_w_pre=d[2])
+    assert all(bool((t == 0).all()) for t in d)
+    with pytest.raises(ValueError, match="shape"):
+        rx.rx_residual_norm([none()], None, torch.ones(2, 72, dtype=dtype, device="cuda"), None, None, none(), None)

@@ -169,3 +169,42 @@ def test_norm_without_rows_keeps_the_gate(gate_len, dtype):
     assert all(bool((t == 0).all()) for t in d)
     with pytest.raises(ValueError, match="shape"):
         rx.rx_residual_norm([none()], None, torch.ones(2, 72, dtype=dtype, device="cuda"), None, None, none(), None)
+
+
+# ---- promises of aliasing ---------------------------------------------------------------
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("post", [True, False])
+@pytest.mark.parametrize("rows,hidden,nsrc", [(3, 7, 2), (40, 520, 3), (300, 1001, 2), (4, 5001, 9), (2, 20003, 2), (2, 32768, 5)])
+def test_norm_in_place(rows, hidden, nsrc, post, dtype):
+    """out_h in any source or the residual, d_residual in d_h: the same bits as in buffers of their own."""
+    g = gen(rows + hidden)
+    t, _ = norm_case(g, rows, hidden, nsrc, dtype, post, 1)
+    mat = lambda v: put(Strided(rows, hidden, dtype, extra=3), v)
+    gate, wp, wz = (gpu(t[k]) for k in ("gate", "w_post", "w_pre"))
+    p, q = torch.empty(rows, device="cuda"), torch.empty(rows, device="cuda")
+
+    def forward(into):
+        ts = [mat(v) for v in (*t["srcs"], t["residual"])]
+        h, z = Strided(rows, hidden, dtype).t if into is None else ts[into], Strided(rows, hidden, dtype).t
+        rx.rx_residual_norm(ts[:-1], ts[-1], gate, wp, wz, h, z, rstd_post=p if post else None, rstd_pre=q, gate_rows=1)
+        return h, z
+
+    h, z = forward(None)
+    for into in range(nsrc + 1):
+        got_h, got_z = forward(into)
+        assert torch.equal(got_h, h) and torch.equal(got_z, z), into
+
+    d_h, d_z = randn(g, rows, hidden, dtype=dtype), randn(g, rows, hidden, dtype=dtype)
+    ws = torch.empty(rx.rx_residual_norm_backward_workspace(rows, hidden, 1), dtype=torch.uint8, device="cuda")
+    srcs, res = [mat(s) for s in t["srcs"]], mat(t["residual"])
+
+    def backward(in_place):
+        dh, ds = mat(d_h), mat(torch.zeros_like(d_h))
+        dr = dh if in_place else mat(torch.zeros_like(d_h))
+        grads = [torch.empty(s, device="cuda") for s in ((rows, hidden), (hidden,), (hidden,))]
+        rx.rx_residual_norm_backward(srcs, res, gate, wp, wz, p if post else None, q, dh, mat(d_z), ds, dr, d_gate=grads[0],
+                                     d_w_post=grads[1] if post else None, d_w_pre=grads[2], gate_rows=1, workspace=ws)
+        return [ds, dr, grads[0], grads[2]] + grads[1:2] * post
+
+    assert all(torch.equal(a, b) for a, b in zip(backward(True), backward(False)))

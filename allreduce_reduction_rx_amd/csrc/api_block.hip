@@ -38,6 +38,9 @@ size_t gate_rows_or_one(size_t gate_rows, size_t rows)
 
 extern "C" {
 
+// Above kDispatchCountAll pairs a caller always brings one, also up to the
+// number that the placing kernel still counts by itself (moe.hip), so that this
+// limit can move without a caller's noticing.
 size_t rx_moe_dispatch_workspace(size_t tokens, int topk, int experts)
 {
     if (!dispatch_sizes_ok(tokens, topk, experts) || tokens * (size_t)topk <= kDispatchCountAll)

@@ -322,7 +322,9 @@ size_t rx_allreduce_local_workspace(int nsrc, size_t count, int block);
  *     see rx_gemm_i8) nor written.
  *   - Outputs must not overlap inputs or each other except where stated.
  *   - Pointers to data without elements may be NULL.
- *   - rows, tokens < 2^22; the number of threads of one launch is limited.
+ *   - rows, tokens < 2^22 (rows of rx_moe_combine's buffers: < 2^31), hidden up
+ *     to 2^30 and ld up to 2^36 elements, unless stated: the number of threads
+ *     of one launch is limited, and row offsets stay far inside 64 bits.
  *   - Results do not depend on timing: no floating-point sum is formed in an
  *     order that could change between two calls.
  * ---------------------------------------------------------------------------
@@ -348,7 +350,8 @@ size_t rx_allreduce_local_workspace(int nsrc, size_t count, int block);
  * gather's gradient with respect to x is rx_moe_combine of d_rows with
  * weights == NULL.
  *
- * tokens topk < 2^31; topk 1 .. RX_MAX_TOPK; experts 1 .. RX_MAX_EXPERTS;
+ * tokens topk < 2^31 (< 2^22 where rx_quant_i8, rx_gemm_i8 or rx_residual_norm
+ * take the sorted rows); topk 1 .. RX_MAX_TOPK; experts 1 .. RX_MAX_EXPERTS;
  * first_expert >= 0. workspace: rx_moe_dispatch_workspace() bytes, 4-byte
  * aligned (NULL where that is 0); its contents on return are unspecified.
  */
@@ -371,6 +374,7 @@ size_t rx_moe_dispatch_workspace(size_t tokens, int topk, int experts);
  * without pairs gets zeros. weights == NULL: all ones.
  *
  * rows, out : RX_FP32 or RX_BF16 (the same); weights: FP32, tokens x topk.
+ * tokens ceil(hidden / 256) < 2^26.
  */
 rx_status_t rx_moe_combine(const void* rows, size_t ld_rows, size_t nrows,
                            const int* slots, const float* weights,
@@ -416,7 +420,9 @@ rx_status_t rx_moe_combine_backward(const void* d_out, size_t ld_d_out,
  *                       the backward pass (p only when w_post is given, q
  *                       only when out_z is).
  * eps                 : positive and finite.
- * A row that is all zero gives u = 0 (or z = 0).
+ * hidden              : up to 32768.
+ * A row that is all zero gives u = 0 (or z = 0). The sum of a row's squares
+ * must be an FP32 value: elements of up to about 1e17 at the largest widths.
  */
 rx_status_t rx_residual_norm(const void* const* srcs, int nsrc, size_t ld_src,
                              const void* residual, size_t ld_residual,
@@ -493,7 +499,9 @@ rx_status_t rx_quant_i8(const void* x, size_t ld_x, size_t rows, size_t k,
  *              anything.
  * k          : up to 131071 (the exact sum fits 32 bits); k == 0 gives zeros.
  * out        : RX_FP32 or RX_BF16.
- * rows < 2^31, n < 2^31. Offsets outside 0 .. rows are clamped to that range.
+ * rows < 2^22, n < 2^31, and fewer than 2^23 - 16 tiles of 256 x 256 outputs with
+ * a partial one for every expert: (rows / 256 + experts + 1) ceil(n / 256).
+ * Offsets outside 0 .. rows are clamped to that range.
  */
 rx_status_t rx_gemm_i8(const void* a, size_t ld_a, const float* a_scales,
                        const void* b, size_t ld_b, size_t stride_b,

@@ -2,8 +2,9 @@
 // operators around a block's allreduce: tensors in, a status out. In C++
 // because these calls are also made for single tokens: rx_moe_dispatch with its
 // seven tensors takes the host 4.1 us this way and took 9.6 us in Python (3.3 us
-// of it the kernel's launch), rx_residual_norm over eight sources 4.0 and 14.6. Raises ValueError or TypeError for what the C entry points cannot
-// see (shapes, devices, contiguity); computes nothing.
+// of it the kernel's launch), rx_residual_norm over eight sources 4.1 and 14.6.
+// Raises ValueError or TypeError for what the C entry points cannot see (shapes,
+// devices, contiguity); computes nothing.
 #include <torch/csrc/autograd/python_variable.h>
 #include <torch/csrc/Exceptions.h>
 

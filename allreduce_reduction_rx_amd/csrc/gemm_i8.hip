@@ -294,9 +294,12 @@ __device__ __forceinline__ void write_results(const GemmI8Args& a, const TileRow
 // read is over half a stage before its end and its buffer is filled again a
 // whole stage before it is needed.
 //
-// What bounds it: power. At 8192^3 in 256 x 256 tiles (439 us, 2.50 POP/s; a
-// large library product reaches 2.44) the clock falls from 2.4 to 1.7 GHz, and
-// what saves instructions and bytes saves time: products of 16 x 16 x 64
+// What bounds it. At 8192^3 in 256 x 256 tiles, the same operands over and over,
+// the clock falls from 2.4 to 1.9 GHz with the matrix cores busy 68% of the
+// cycles: power (393 to 447 us from card to card, 2.80 to 2.46 POP/s; a large library
+// product reaches 2.54 to 2.44). With operands that are in no cache it stays at
+// 2.2 GHz, busy 53% (457 us): the start of each of four rounds waits for memory
+// too. What saves instructions and bytes saved time: products of 16 x 16 x 64
 // move half the accumulators a multiply that 32 x 32 x 32 do (494 against 510
 // us before the earlier refill), 128-byte stages half the requests of 64-byte
 // ones, eight waves of 64 x 128 keep all fragments in registers.

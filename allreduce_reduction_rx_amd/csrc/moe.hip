@@ -293,8 +293,8 @@ __global__ __launch_bounds__(256) void k_dispatch_rows(DispatchArgs a)
 // A pair's place is the number of (expert, pair) keys below its own: one
 // comparison and one addition of a carry for an id. The loop over the ids stays
 // rolled: at these sizes a kernel's time is its way through code that no
-// instruction cache holds yet (16 ids at a time, unrolled: 8.4 us where 32
-// tokens take 6.2).
+// instruction cache holds yet (32 tokens x 8 choices x 8192 BF16 took 8.4 us with
+// 16 ids at a time, unrolled, 6.2 rolled, and take 4.1 us in this form).
 constexpr int kPairBits = 12;
 static_assert(kDispatchCountAll <= 1 << kPairBits, "a key holds the pair's number");
 

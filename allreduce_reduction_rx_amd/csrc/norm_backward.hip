@@ -15,8 +15,8 @@
 //
 // The next row's loads go out as soon as this row's are unpacked, before the
 // sums, the results and the stores of this row: 80 KiB in flight a CU. HBM
-// bound: 16384 x 8192 BF16 over two sources takes 366 us for 1.88 GB read and
-// written (5.1 TB/s, what a large copy reaches).
+// bound: 16384 x 8192 BF16 over two sources takes 370 us for 1.88 GB read and
+// written (5.1 TB/s; large copies reach 5.0 to 5.8).
 //
 // MULTI: the part may see several gate rows. A gate row whose rows all lie in
 // the part is written at once; one that crosses the part's start goes to
@@ -26,7 +26,9 @@
 // backward: 296 us, 344 with 1024 threads), and all rows of 1537 to 2048, where
 // 1024 threads leave 128 registers a thread and nothing is loaded ahead (4096 x
 // 16384 BF16: 432 us, against 717 us with four vectors a thread loaded ahead and
-// 807 us with k_norm_backward_long, which takes the rows above).
+// 807 us with k_norm_backward_long, which takes the rows above; 457 with inputs
+// that are in no cache, 323 of them this direction's). Both are far from the memory:
+// 4096 rows of FP32 take 224 us at 8192 (1024 threads) and 640 at 16384 (long).
 #include "norm_common.hpp"
 
 namespace rx {

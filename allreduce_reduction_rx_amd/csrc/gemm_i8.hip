@@ -130,7 +130,9 @@ __device__ __forceinline__ TileRows find_tile(const GemmI8Args& a, const Tiles& 
         return {lo, lo + bm < a.rows ? lo + bm : a.rows, -1};
     }
     uint32_t base = 0, lo = t.lo, hi = t.hi, incl = t.incl;
-    for (int e0 = 0;;) {
+    // offsets past the first 64 are read a second time: should another stream
+    // write them meanwhile, the walk still ends, without a tile
+    for (int e0 = 0; e0 < a.experts;) {
         const uint64_t past = __ballot(base + incl > tm);
         if (past) {
             const int l = __builtin_ctzll(past);
@@ -145,6 +147,7 @@ __device__ __forceinline__ TileRows find_tile(const GemmI8Args& a, const Tiles& 
         e0 += kWave;
         incl = tiles_to(a, e0 + lane_id(), bm, lo, hi);
     }
+    return {0, 0, 0};
 }
 
 constexpr uint32_t kTileGroup = 8;

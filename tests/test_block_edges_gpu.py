@@ -208,3 +208,23 @@ def test_norm_in_place(rows, hidden, nsrc, post, dtype):
         return [ds, dr, grads[0], grads[2]] + grads[1:2] * post
 
     assert all(torch.equal(a, b) for a, b in zip(backward(True), backward(False)))
+
+
+# ---- products: more experts than a wave has lanes -------------------------------------------
+
+@pytest.mark.parametrize("experts,every,most", [(64, 1, 3), (65, 64, 40), (128, 127, 300), (1024, 1, 2), (1000, 333, 70)])
+def test_gemm_of_many_experts(experts, every, most):
+    """Experts with and without rows past the first 64, whose offsets are looked up in turns."""
+    g = gen(experts)
+    counts = [int(torch.randint(0, most + 1, (1,), generator=g)) if e % every == 0 or e == experts - 1 else 0 for e in range(experts)]
+    rows, n, k = sum(counts) + 3, 24, 40
+    offsets = torch.tensor([0] + counts).cumsum(0).to(torch.int32)
+    a, b = (torch.randint(-127, 128, s, generator=g).to(torch.int8) for s in ((rows, 48), (experts, n, 48)))
+    out = Strided(rows, n, FP32)
+    rx.rx_gemm_i8(gpu(a)[:, :k], torch.ones(rows, device="cuda"), gpu(b)[:, :, :k], torch.ones(experts, n, device="cuda"), out.t,
+                  offsets=gpu(offsets))
+    expert = torch.repeat_interleave(torch.arange(experts), torch.tensor(counts))
+    want = torch.zeros(rows, n, dtype=torch.float64)
+    want[:-3] = (b[expert][:, :, :k].double() * a[:-3, None, :k].double()).sum(2)
+    assert torch.equal(out.t.cpu().double(), want)   # sums below 2^24: exact in float32
+    out.check()

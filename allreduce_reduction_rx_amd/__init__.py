@@ -29,7 +29,9 @@ __all__ = [
     "RX_ALGO_LOWPREC", "EXPORTED_SYMBOLS", "RX_INT8", "RX_MAX_TOPK", "RX_MAX_EXPERTS",
     "rx_moe_dispatch", "rx_moe_dispatch_workspace", "rx_moe_combine", "rx_moe_combine_backward",
     "rx_residual_norm", "rx_residual_norm_backward", "rx_residual_norm_backward_workspace",
-    "rx_quant_i8", "rx_gemm_i8",
+    "rx_quant_i8", "rx_gemm_i8", "rx_moe_route", "rx_moe_route_workspace", "rx_moe_route_backward",
+    "rx_quant_fp4", "rx_gemm_fp4", "rx_layer_norm", "rx_layer_norm_backward",
+    "rx_layer_norm_backward_workspace",
 ]
 
 RX_FP32, RX_BF16, RX_FP8_E4M3, RX_FP8_E5M2, RX_INT8 = 0, 1, 2, 3, 4
@@ -48,7 +50,9 @@ EXPORTED_SYMBOLS = (
     "rxtest_group_max", "rxtest_stream", "rxtest_stream_sink_bytes", "rxtest_stream_mixed",
     "rxtest_copy_streams", "rx_moe_dispatch", "rx_moe_dispatch_workspace", "rx_moe_combine",
     "rx_moe_combine_backward", "rx_residual_norm", "rx_residual_norm_backward",
-    "rx_residual_norm_backward_workspace", "rx_quant_i8", "rx_gemm_i8",
+    "rx_residual_norm_backward_workspace", "rx_quant_i8", "rx_gemm_i8", "rx_moe_route",
+    "rx_moe_route_workspace", "rx_moe_route_backward", "rx_quant_fp4", "rx_gemm_fp4", "rx_layer_norm",
+    "rx_layer_norm_backward", "rx_layer_norm_backward_workspace",
 )
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -111,6 +115,14 @@ def lib() -> ctypes.CDLL:
                                           _P, _SZ, _P],
             "rx_quant_i8": [_P, _SZ, _SZ, _SZ, _I, _P, _SZ, _P, _P],
             "rx_gemm_i8": [_P, _SZ, _P, _P, _SZ, _SZ, _P, _P, _I, _SZ, _SZ, _SZ, _P, _SZ, _I, _P],
+            "rx_moe_route": [_P, _SZ, _P, _SZ, _I, _I, _I, _I, _P, _P, _P, _P, _P, _P, _SZ, _P],
+            "rx_moe_route_backward": [_P, _SZ, _P, _P, _P, _P, _P, _SZ, _I, _I, _I, _I, _P, _SZ, _P],
+            "rx_quant_fp4": [_P, _SZ, _SZ, _SZ, _I, _I, _P, _SZ, _P, _P],
+            "rx_gemm_fp4": [_P, _SZ, _P, _SZ, _SZ, _P, _I, _P, _I, _SZ, _SZ, _SZ, _I, _P, _SZ, _P],
+            "rx_layer_norm": [_PP, _I, _SZ, _P, _P, _SZ, _P, _P, _F, _F, _P, _SZ, _SZ, _I, _P, _SZ, _P,
+                              _SZ, _P, _P, _P],
+            "rx_layer_norm_backward": [_P, _SZ, _P, _P, _P, _F, _P, _SZ, _SZ, _I, _P, _SZ, _P, _SZ, _P,
+                                       _SZ, _P, _SZ, _P, _P, _P, _P, _SZ, _P],
             "rxtest_fp8_encode_bits": [ctypes.c_uint32, _SZ, _I, _P, _P],
             "rxtest_block_scale_bits": [ctypes.c_uint32, _SZ, _I, _P, _P, _P],
             "rxtest_fp8_decode": [_P, _SZ, _I, _P, _P],
@@ -132,6 +144,10 @@ def lib() -> ctypes.CDLL:
         L.rx_moe_dispatch_workspace.restype = ctypes.c_size_t
         L.rx_residual_norm_backward_workspace.argtypes = [_SZ, _SZ, _SZ]
         L.rx_residual_norm_backward_workspace.restype = ctypes.c_size_t
+        L.rx_moe_route_workspace.argtypes = [_SZ, _I]
+        L.rx_moe_route_workspace.restype = ctypes.c_size_t
+        L.rx_layer_norm_backward_workspace.argtypes = [_SZ, _SZ]
+        L.rx_layer_norm_backward_workspace.restype = ctypes.c_size_t
         L.rx_status_string.argtypes = [_I]
         L.rx_status_string.restype = ctypes.c_char_p
         _lib = L
@@ -402,7 +418,8 @@ def _bind():
         spec.loader.exec_module(m)
         m.connect(torch._C._cuda_getCurrentRawStream, *(ctypes.cast(fn, ctypes.c_void_p).value for fn in (
             L.rx_moe_dispatch, L.rx_moe_combine, L.rx_moe_combine_backward, L.rx_residual_norm,
-            L.rx_residual_norm_backward, L.rx_quant_i8, L.rx_gemm_i8)))
+            L.rx_residual_norm_backward, L.rx_quant_i8, L.rx_gemm_i8, L.rx_moe_route, L.rx_moe_route_backward,
+            L.rx_quant_fp4, L.rx_gemm_fp4, L.rx_layer_norm, L.rx_layer_norm_backward)))
         _bound = m
     return _bound
 
@@ -485,6 +502,71 @@ def rx_gemm_i8(a, a_scales, b, b_scales, out, offsets=None, stream=None) -> None
     rx_moe_dispatch) b (experts x n x k), rows offsets[e] .. offsets[e + 1] - 1
     times b[e]. Row strides are multiples of 16 (pad the rows)."""
     _check((_bound or _bind()).gemm_i8(*_here(stream), a, a_scales, b, b_scales, out, offsets), "rx_gemm_i8")
+
+
+# ---- before and behind the experts, and 4-bit weights -------------------------
+
+def rx_moe_route_workspace(tokens: int, experts: int) -> int:
+    """Workspace bytes of rx_moe_route where counts and losses are wanted."""
+    return int(lib().rx_moe_route_workspace(tokens, experts))
+
+
+def rx_moe_route(logits, expert_ids, weights, token_mask=None, renormalize: bool = False, lse=None,
+                 counts=None, losses=None, workspace=None, stream=None) -> None:
+    """The topk experts of each token (expert_ids int32 and weights float32, tokens
+    x topk) from the router's logits (tokens x experts): softmax, with renormalize
+    over the chosen ones. token_mask (bool or uint8): tokens to leave out. lse
+    (float32, tokens) is what the backward pass needs; counts (int32, experts + 1,
+    the last the tokens) and losses (float32: balance, mean of lse^2) come together,
+    with a workspace."""
+    _check((_bound or _bind()).moe_route(*_here(stream), logits, expert_ids, weights, token_mask, renormalize,
+                                         lse, counts, losses, workspace), "rx_moe_route")
+
+
+def rx_moe_route_backward(logits, expert_ids, lse, counts, d_weights, d_losses, d_logits,
+                          renormalize: bool = False, stream=None) -> None:
+    """Gradient of rx_moe_route: d_logits from d_weights (float32, tokens x topk) and
+    d_losses (float32, 2, on the GPU); either may be None, and counts with d_losses."""
+    _check((_bound or _bind()).moe_route_backward(*_here(stream), logits, expert_ids, lse, counts, d_weights,
+                                                  d_losses, d_logits, renormalize), "rx_moe_route_backward")
+
+
+def rx_quant_fp4(x, codes, scales, group: int, stream=None) -> None:
+    """Rows of x (float32 or bfloat16, rows x k) to E2M1 codes, two a byte (uint8, rows x
+    ceil(k / 2)), and a float32 scale for each group of 32, 64 or 128 (rows x ceil(k /
+    group)). For rx_gemm_fp4 the rows of codes are padded to multiples of 16 bytes."""
+    _check((_bound or _bind()).quant_fp4(*_here(stream), x, codes, scales, group), "rx_quant_fp4")
+
+
+def rx_gemm_fp4(a, b, b_scales, out, group: int, offsets=None, stream=None) -> None:
+    """out[m, j] = sum over i of a[m, i] (b[j, i] times its group's scale), for a (rows x
+    k, float32 or bfloat16, any stride) and rx_quant_fp4's codes b (n x ceil(k / 2)) and
+    scales, or with offsets (int32, experts + 1, of rx_moe_dispatch) a matrix for each
+    expert. b's row strides are multiples of 16 (pad the rows)."""
+    _check((_bound or _bind()).gemm_fp4(*_here(stream), a, b, b_scales, out, group, offsets), "rx_gemm_fp4")
+
+
+def rx_layer_norm(srcs: Sequence, residual, w, b, out_h, out_z, bias=None, mean=None, rstd=None,
+                  drop: float = 0.0, rng=None, eps: float = 1e-5, stream=None) -> None:
+    """h = residual + dropout(sum of srcs + bias), z = layer norm of h as it is stored,
+    times w plus b. residual, w, b, bias and one of out_h, out_z may be None. rng
+    (int64, 2, on the GPU): seed and offset of dropout's generator."""
+    _check((_bound or _bind()).layer_norm(*_here(stream), srcs, residual, w, b, out_h, out_z, bias, mean, rstd,
+                                          drop, rng, eps), "rx_layer_norm")
+
+
+def rx_layer_norm_backward_workspace(rows: int, hidden: int) -> int:
+    """Workspace bytes of rx_layer_norm_backward."""
+    return int(lib().rx_layer_norm_backward_workspace(rows, hidden))
+
+
+def rx_layer_norm_backward(h, w, mean, rstd, d_h, d_z, d_src, d_residual=None, d_bias=None, d_w=None,
+                           d_b=None, drop: float = 0.0, rng=None, workspace=None, stream=None) -> None:
+    """Gradient of rx_layer_norm from d_h and d_z (either may be None), the h it wrote,
+    its mean and rstd, and the same drop and rng: d_src (every source's), d_residual,
+    and in float32 d_bias, d_w, d_b; each of the five may be None."""
+    _check((_bound or _bind()).layer_norm_backward(*_here(stream), h, w, mean, rstd, d_h, d_z, d_src, d_residual,
+                                                   d_bias, d_w, d_b, drop, rng, workspace), "rx_layer_norm_backward")
 
 
 # ---- test hooks (rx_testhooks.h) -------------------------------------------

@@ -9,20 +9,6 @@ namespace {
 
 using namespace rx;
 
-// Rows and tokens of one call: a workgroup of up to 1024 threads each, and a
-// launch has fewer than 2^32 threads.
-constexpr size_t kMaxRows = ((size_t)1 << 22) - 1;
-constexpr size_t kMaxLd = (size_t)1 << 36;   // row offsets stay far inside 64 bits
-constexpr size_t kMaxGemmLd = (size_t)1 << 23;   // a tile's 256 rows lie within 32 bits
-constexpr size_t kMaxHidden = (size_t)1 << 30;
-
-size_t elem_size(rx_dtype_t t) { return t == RX_BF16 ? 2 : t == RX_INT8 ? 1 : 4; }
-bool element_aligned(const void* p, rx_dtype_t t) { return ((uintptr_t)p & (elem_size(t) - 1)) == 0; }
-int dt_index(rx_dtype_t t) { return t == RX_BF16 ? 1 : 0; }
-bool bad_ld(size_t ld, size_t len) { return ld < len || ld > kMaxLd; }
-// a row stride matters only where there is a second row
-bool bad_ld(size_t ld, size_t len, size_t rows) { return rows > 1 ? bad_ld(ld, len) : ld > kMaxLd; }
-
 bool dispatch_sizes_ok(size_t tokens, int topk, int experts)
 {
     return topk >= 1 && topk <= kMaxTopk && experts >= 1 && experts <= kMaxExperts && tokens <= kMaxRows &&

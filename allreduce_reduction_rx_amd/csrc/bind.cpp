@@ -25,7 +25,14 @@ struct {
     decltype(&rx_residual_norm_backward) residual_norm_backward;
     decltype(&rx_quant_i8) quant_i8;
     decltype(&rx_gemm_i8) gemm_i8;
+    decltype(&rx_moe_route) moe_route;
+    decltype(&rx_moe_route_backward) moe_route_backward;
+    decltype(&rx_quant_fp4) quant_fp4;
+    decltype(&rx_gemm_fp4) gemm_fp4;
+    decltype(&rx_layer_norm) layer_norm;
+    decltype(&rx_layer_norm_backward) layer_norm_backward;
 } rx;
+constexpr int kEntries = sizeof(rx) / sizeof(void*);
 
 template <class... A>
 [[noreturn]] void refuse(PyObject* type, const char* format, A... a)
@@ -461,16 +468,214 @@ int gemm_i8(PyObject* const* a, Py_ssize_t n)
                       cols, k, out.data_ptr(), ld_o, dt, stream);
 }
 
+bool truth(PyObject* o)
+{
+    const int v = PyObject_IsTrue(o);
+    if (v < 0)
+        throw Raised();
+    return v != 0;
+}
+
+int moe_route(PyObject* const* a, Py_ssize_t n)
+{
+    const Where w = where(a, n, 11);
+    const at::Tensor &logits = tensor(a[2], "logits"), &ids = tensor(a[3], "expert_ids"), &weights = tensor(a[4], "weights");
+    two_dims(logits, "logits");
+    two_dims(ids, "expert_ids");
+    const int64_t tokens = logits.size(0), experts = logits.size(1), topk = ids.size(1);
+    if (experts > INT32_MAX || topk > INT32_MAX)
+        refuse(PyExc_ValueError, "too many experts");
+    const rx_dtype_t dt = data_type(logits);
+    const size_t ld = block(w.dev, logits.scalar_type(), {tokens, experts}, "logits", logits);
+    int* pi = (int*)packed(w.dev, at::kInt, {tokens, topk}, "expert_ids", ids);
+    float* pw = (float*)packed(w.dev, at::kFloat, {tokens, topk}, "weights", weights);
+    const unsigned char* mask = nullptr;
+    if (given(a[5])) {
+        const at::Tensor& m = tensor(a[5], "token_mask");
+        const at::ScalarType type = m.scalar_type() == at::kByte ? at::kByte : at::kBool;
+        mask = (const unsigned char*)packed(w.dev, type, {tokens}, "token_mask", m);
+    }
+    const bool renormalize = truth(a[6]);
+    float* lse = (float*)packed(w.dev, at::kFloat, {tokens}, "lse", a[7]);
+    int* counts = (int*)packed(w.dev, at::kInt, {experts + 1}, "counts", a[8]);
+    float* losses = (float*)packed(w.dev, at::kFloat, {2}, "losses", a[9]);
+    size_t bytes;
+    void* ws = workspace(w.dev, a[10], &bytes);
+    const hipStream_t stream = w.stream();
+    NoGil open;
+    return rx.moe_route(logits.data_ptr(), ld, mask, tokens, (int)experts, (int)topk, renormalize, dt, pi, pw, lse, counts, losses,
+                        ws, bytes, stream);
+}
+
+int moe_route_backward(PyObject* const* a, Py_ssize_t n)
+{
+    const Where w = where(a, n, 10);
+    const at::Tensor &logits = tensor(a[2], "logits"), &ids = tensor(a[3], "expert_ids"), &d = tensor(a[8], "d_logits");
+    two_dims(logits, "logits");
+    two_dims(ids, "expert_ids");
+    const int64_t tokens = logits.size(0), experts = logits.size(1), topk = ids.size(1);
+    if (experts > INT32_MAX || topk > INT32_MAX)
+        refuse(PyExc_ValueError, "too many experts");
+    const rx_dtype_t dt = data_type(logits);
+    const size_t ld = block(w.dev, logits.scalar_type(), {tokens, experts}, "logits", logits);
+    const int* pi = (const int*)packed(w.dev, at::kInt, {tokens, topk}, "expert_ids", ids);
+    const float* lse = (const float*)packed(w.dev, at::kFloat, {tokens}, "lse", tensor(a[4], "lse"));
+    const int* counts = (const int*)packed(w.dev, at::kInt, {experts + 1}, "counts", a[5]);
+    const float* dw = (const float*)packed(w.dev, at::kFloat, {tokens, topk}, "d_weights", a[6]);
+    const float* dl = (const float*)packed(w.dev, at::kFloat, {2}, "d_losses", a[7]);
+    const size_t ld_d = block(w.dev, logits.scalar_type(), {tokens, experts}, "d_logits", d);
+    const bool renormalize = truth(a[9]);
+    const hipStream_t stream = w.stream();
+    NoGil open;
+    return rx.moe_route_backward(logits.data_ptr(), ld, pi, lse, counts, dw, dl, tokens, (int)experts, (int)topk, renormalize, dt,
+                                 d.data_ptr(), ld_d, stream);
+}
+
+int64_t groups_of(int64_t k, int group)
+{
+    if (group < 1)
+        refuse(PyExc_ValueError, "group must be positive");
+    return (k + group - 1) / group;
+}
+
+int quant_fp4(PyObject* const* a, Py_ssize_t n)
+{
+    const Where w = where(a, n, 6);
+    const at::Tensor &x = tensor(a[2], "x"), &codes = tensor(a[3], "codes"), &scales = tensor(a[4], "scales");
+    two_dims(x, "x");
+    const int group = integer32(a[5], "group");
+    const int64_t rows = x.size(0), k = x.size(1);
+    const rx_dtype_t dt = data_type(x);
+    const size_t ld_x = block(w.dev, x.scalar_type(), {rows, k}, "x", x);
+    const size_t ld_c = block(w.dev, at::kByte, {rows, (k + 1) / 2}, "codes", codes);
+    float* ps = (float*)packed(w.dev, at::kFloat, {rows, groups_of(k, group)}, "scales", scales);
+    const hipStream_t stream = w.stream();
+    NoGil open;
+    return rx.quant_fp4(x.data_ptr(), ld_x, rows, k, dt, group, codes.data_ptr(), ld_c, ps, stream);
+}
+
+int gemm_fp4(PyObject* const* a, Py_ssize_t n)
+{
+    const Where w = where(a, n, 8);
+    const at::Tensor &ta = tensor(a[2], "a"), &tb = tensor(a[3], "b"), &out = tensor(a[5], "out");
+    two_dims(ta, "a");
+    const int group = integer32(a[6], "group");
+    const bool grouped = given(a[7]);
+    if (tb.dim() != (grouped ? 3 : 2))
+        refuse(PyExc_ValueError, "b must have %s dimensions", grouped ? "three" : "two");
+    const int64_t rows = ta.size(0), k = ta.size(1), half = (k + 1) / 2, cols = tb.size(-2), experts = grouped ? tb.size(0) : 1;
+    const int64_t groups = groups_of(k, group);
+    if (experts > INT32_MAX)
+        refuse(PyExc_ValueError, "too many experts");
+    const rx_dtype_t dt = data_type(ta);
+    const size_t ld_a = block(w.dev, ta.scalar_type(), {rows, k}, "a", ta);
+    size_t ld_b, stride_b = 0;
+    const int* offsets = nullptr;
+    const float* sb;
+    if (grouped) {
+        ld_b = chunked(block(w.dev, at::kByte, {experts, cols, half}, "b", tb), tb, half);
+        offsets = (const int*)packed(w.dev, at::kInt, {experts + 1}, "offsets", a[7]);
+        if (tb.stride(0) < 0)
+            refuse(PyExc_ValueError, "b's matrices must follow each other");
+        stride_b = experts > 1 && tb.numel() > 0 ? (size_t)tb.stride(0) : 0;
+        sb = (const float*)packed(w.dev, at::kFloat, {experts, cols, groups}, "b_scales", tensor(a[4], "b_scales"));
+    } else {
+        ld_b = chunked(block(w.dev, at::kByte, {cols, half}, "b", tb), tb, half);
+        sb = (const float*)packed(w.dev, at::kFloat, {cols, groups}, "b_scales", tensor(a[4], "b_scales"));
+    }
+    const size_t ld_o = block(w.dev, ta.scalar_type(), {rows, cols}, "out", out);
+    check_padded(tb, half, "b");
+    const hipStream_t stream = w.stream();
+    NoGil open;
+    return rx.gemm_fp4(ta.data_ptr(), ld_a, tb.data_ptr(), ld_b, stride_b, sb, group, offsets, (int)experts, rows, cols, k, dt,
+                       out.data_ptr(), ld_o, stream);
+}
+
+// Seed and offset of dropout's generator.
+const unsigned long long* generator(int dev, PyObject* o)
+{
+    return (const unsigned long long*)packed(dev, at::kLong, {2}, "rng", o);
+}
+
+void* matrix(int dev, at::ScalarType type, Sizes shape, const char* name, PyObject* o, size_t* ld)
+{
+    *ld = 0;
+    if (!given(o))
+        return nullptr;
+    const at::Tensor& t = tensor(o, name);
+    *ld = block(dev, type, shape, name, t);
+    return t.data_ptr();
+}
+
+int layer_norm(PyObject* const* a, Py_ssize_t n)
+{
+    const Where w = where(a, n, 14);
+    // the sources as for the residual norm, without its other operands
+    PyObject* const args[] = {a[2], a[3], Py_None, Py_None, Py_None, Py_None};
+    const NormInputs in = norm_inputs(w.dev, args);
+    const Sizes row = {in.hidden};
+    const void *pw = packed(w.dev, in.type, row, "w", a[4]), *pb = packed(w.dev, in.type, row, "b", a[5]);
+    size_t ld_h, ld_z;
+    void *h = norm_matrix(w.dev, in, "out_h", a[6], &ld_h), *z = norm_matrix(w.dev, in, "out_z", a[7], &ld_z);
+    const void* bias = packed(w.dev, in.type, row, "bias", a[8]);
+    float *mean = (float*)packed(w.dev, at::kFloat, {in.rows}, "mean", a[9]),
+          *rstd = (float*)packed(w.dev, at::kFloat, {in.rows}, "rstd", a[10]);
+    const float drop = real(a[11]), eps = real(a[13]);
+    const unsigned long long* rng = generator(w.dev, a[12]);
+    const hipStream_t stream = w.stream();
+    NoGil open;
+    return rx.layer_norm(in.src, in.nsrc, in.ld_src, bias, in.residual, in.ld_residual, pw, pb, eps, drop, rng, in.rows, in.hidden,
+                         in.dtype, h, ld_h, z, ld_z, mean, rstd, stream);
+}
+
+// a: h, w, mean, rstd, d_h, d_z, d_src, d_residual, d_bias, d_w, d_b, drop, rng,
+// workspace. The first matrix that is given says what the others are.
+int layer_norm_backward(PyObject* const* a, Py_ssize_t n)
+{
+    const Where w = where(a, n, 16);
+    const char* const names[] = {"h", "d_h", "d_z", "d_src", "d_residual"};
+    PyObject* const given_as[] = {a[2], a[6], a[7], a[8], a[9]};
+    const at::Tensor* first = nullptr;
+    for (int i = 0; i < 5 && !first; ++i)
+        if (given(given_as[i])) {
+            first = &tensor(given_as[i], names[i]);
+            two_dims(*first, names[i]);
+        }
+    if (!first)
+        refuse(PyExc_ValueError, "no gradient is given or wanted");
+    const int64_t rows = first->size(0), hidden = first->size(1);
+    const at::ScalarType type = first->scalar_type();
+    const rx_dtype_t dt = data_type(*first);
+    size_t ld[5];
+    void* m[5];
+    for (int i = 0; i < 5; ++i)
+        m[i] = matrix(w.dev, type, {rows, hidden}, names[i], given_as[i], &ld[i]);
+    const void* pw = packed(w.dev, type, {hidden}, "w", a[3]);
+    const float *mean = (const float*)packed(w.dev, at::kFloat, {rows}, "mean", a[4]),
+                *rstd = (const float*)packed(w.dev, at::kFloat, {rows}, "rstd", a[5]);
+    float *d_bias = (float*)packed(w.dev, at::kFloat, {hidden}, "d_bias", a[10]),
+          *d_w = (float*)packed(w.dev, at::kFloat, {hidden}, "d_w", a[11]),
+          *d_b = (float*)packed(w.dev, at::kFloat, {hidden}, "d_b", a[12]);
+    const float drop = real(a[13]);
+    const unsigned long long* rng = generator(w.dev, a[14]);
+    size_t bytes;
+    void* ws = workspace(w.dev, a[15], &bytes);
+    const hipStream_t stream = w.stream();
+    NoGil open;
+    return rx.layer_norm_backward(m[0], ld[0], pw, mean, rstd, drop, rng, rows, hidden, dt, m[1], ld[1], m[2], ld[2], m[3], ld[3],
+                                  m[4], ld[4], d_bias, d_w, d_b, ws, bytes, stream);
+}
+
 // connect(torch's stream lookup, addresses of the entry points in the order
 // of `rx` above)
 int connect(PyObject* const* a, Py_ssize_t n)
 {
-    if (n != 8)
-        refuse(PyExc_TypeError, "a function and 7 addresses");
+    if (n != kEntries + 1)
+        refuse(PyExc_TypeError, "a function and %d addresses", kEntries);
     Py_INCREF(a[0]);
     current_stream = a[0];
     void** to = reinterpret_cast<void**>(&rx);
-    for (int i = 0; i < 7; ++i)
+    for (int i = 0; i < kEntries; ++i)
         to[i] = reinterpret_cast<void*>((intptr_t)integer(a[i + 1]));
     return 0;
 }
@@ -492,6 +697,8 @@ PyObject* entry(PyObject*, PyObject* const* a, Py_ssize_t n)
 PyMethodDef methods[] = {
     RX_ENTRY(connect), RX_ENTRY(moe_dispatch), RX_ENTRY(moe_combine), RX_ENTRY(moe_combine_backward),
     RX_ENTRY(residual_norm), RX_ENTRY(residual_norm_backward), RX_ENTRY(quant_i8), RX_ENTRY(gemm_i8),
+    RX_ENTRY(moe_route), RX_ENTRY(moe_route_backward), RX_ENTRY(quant_fp4), RX_ENTRY(gemm_fp4), RX_ENTRY(layer_norm),
+    RX_ENTRY(layer_norm_backward),
     {nullptr, nullptr, 0, nullptr},
 };
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_rxbind", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};

@@ -179,6 +179,15 @@ __device__ __forceinline__ uint32_t wave_sum_u(uint32_t v)
     return q[0] + q[1];
 }
 
+// What the wave's lanes wrote to LDS is there for all of them: its LDS
+// instructions run in order, so only the compiler has to keep theirs.
+__device__ __forceinline__ void wave_sync()
+{
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
 // Inclusive sum over the lanes up to this one.
 __device__ __forceinline__ uint32_t wave_incl(uint32_t v)
 {

@@ -9,45 +9,6 @@
 namespace rx {
 namespace {
 
-// y = the sources' sum in their order, B sources' loads of a thread in flight
-// together.
-template <int DT, bool TAIL, int NV>
-__device__ __forceinline__ void fold_row(const void* const* src, int nsrc, size_t row_bytes, int hidden,
-                                         float (*y)[Elem<DT>::kVE])
-{
-    constexpr int VE = Elem<DT>::kVE, B = NV == 1 ? 8 : 4;   // more would cost a longer row its occupancy
-    const int tid = (int)threadIdx.x, bd = (int)blockDim.x;
-#pragma unroll
-    for (int u = 0; u < NV; ++u)
-#pragma unroll
-        for (int k = 0; k < VE; ++k)
-            y[u][k] = -0.0f;   // x + -0 = x for every x
-    auto batch = [&](int r) {
-        u32x4 x[B][NV];
-#pragma unroll
-        for (int b = 0; b < B; ++b)
-            if (r + b < nsrc)
-#pragma unroll
-                for (int u = 0; u < NV; ++u)
-                    x[b][u] = ld_raw<DT, TAIL, true>(static_cast<const char*>(src[r + b]) + row_bytes, tid + u * bd, hidden);
-#pragma unroll
-        for (int b = 0; b < B; ++b)
-            if (r + b < nsrc)
-#pragma unroll
-                for (int u = 0; u < NV; ++u) {
-                    float f[VE];
-                    unpack<DT>(fixed<DT, TAIL>(x[b][u], tid + u * bd, hidden), f);
-#pragma unroll
-                    for (int k = 0; k < VE; ++k)
-                        y[u][k] += f[k];
-                }
-    };
-    batch(0);   // its pointers come with the kernel's arguments
-#pragma unroll 1
-    for (int r = B; r < nsrc; r += B)
-        batch(r);
-}
-
 // NV 1: the gate and the weights are loaded before the sources too, so that a
 // row has one round trip to memory (32 rows of 8192 BF16 over 8 sources: 6.0
 // us, 6.6 with two vectors a thread and the weights loaded where they are

@@ -1,5 +1,5 @@
-// norm_common.hpp -- what the two directions of the residual norm share
-// (norm.hip, norm_backward.hip).
+// norm_common.hpp -- what the norms and their gradients share (norm.hip,
+// norm_backward.hip, layer_norm.hip).
 #pragma once
 
 #include "block_common.hpp"
@@ -59,6 +59,45 @@ __device__ __forceinline__ void fold_batch(const void* const* src, int r, size_t
             for (int k = 0; k < VE; ++k)
                 y[u][k] = FIRST && b == 0 ? f[k] : y[u][k] + f[k];
         }
+}
+
+// y = the sources' sum in their order, B sources' loads of a thread in flight
+// together.
+template <int DT, bool TAIL, int NV>
+__device__ __forceinline__ void fold_row(const void* const* src, int nsrc, size_t row_bytes, int hidden,
+                                         float (*y)[Elem<DT>::kVE])
+{
+    constexpr int VE = Elem<DT>::kVE, B = NV == 1 ? 8 : 4;   // more would cost a longer row its occupancy
+    const int tid = (int)threadIdx.x, bd = (int)blockDim.x;
+#pragma unroll
+    for (int u = 0; u < NV; ++u)
+#pragma unroll
+        for (int k = 0; k < VE; ++k)
+            y[u][k] = -0.0f;   // x + -0 = x for every x
+    auto batch = [&](int r) {
+        u32x4 x[B][NV];
+#pragma unroll
+        for (int b = 0; b < B; ++b)
+            if (r + b < nsrc)
+#pragma unroll
+                for (int u = 0; u < NV; ++u)
+                    x[b][u] = ld_raw<DT, TAIL, true>(static_cast<const char*>(src[r + b]) + row_bytes, tid + u * bd, hidden);
+#pragma unroll
+        for (int b = 0; b < B; ++b)
+            if (r + b < nsrc)
+#pragma unroll
+                for (int u = 0; u < NV; ++u) {
+                    float f[VE];
+                    unpack<DT>(fixed<DT, TAIL>(x[b][u], tid + u * bd, hidden), f);
+#pragma unroll
+                    for (int k = 0; k < VE; ++k)
+                        y[u][k] += f[k];
+                }
+    };
+    batch(0);   // its pointers come with the kernel's arguments
+#pragma unroll 1
+    for (int r = B; r < nsrc; r += B)
+        batch(r);
 }
 
 }  // namespace

@@ -165,6 +165,92 @@ struct GemmI8Args {
     int experts;
 };
 
+struct RouteArgs {
+    const void* logits;
+    const uint8_t* mask;         // NULL: all tokens
+    int* ids;
+    float* weights;
+    float* lse;                  // NULL: not wanted
+    int* counts;                 // NULL: no counts and no losses
+    float* losses;
+    uint32_t* workspace;
+    size_t ld, tokens;
+    uint32_t parts;              // workgroups of the first launch
+    int experts, topk, renormalize;
+};
+
+struct RouteBwdArgs {
+    const void* logits;
+    const int* ids;
+    const float* lse;
+    const int* counts;
+    const float* d_weights;
+    const float* d_losses;
+    void* d_logits;
+    size_t ld, ld_d, tokens;
+    int experts, topk, renormalize;
+};
+
+struct LayerNormArgs {
+    const void* src[kMaxSrc];
+    const void* bias;
+    const void* residual;
+    const void* w;
+    const void* b;
+    const unsigned long long* rng;   // seed, offset
+    void* out_h;
+    void* out_z;
+    float* mean;
+    float* rstd;
+    size_t ld_src, ld_residual, ld_h, ld_z;
+    size_t rows, hidden;
+    uint32_t threshold;          // 65536 p; 0: no dropout
+    float gain, eps, inv_hidden;
+    int nsrc;
+};
+
+struct LayerNormBwdArgs {
+    const void* h;
+    const void* w;
+    const float* mean;
+    const float* rstd;
+    const unsigned long long* rng;
+    const void* d_h;
+    const void* d_z;
+    void* d_src;
+    void* d_residual;
+    float* d_bias;
+    float* d_w;
+    float* d_b;
+    float* means;                // workspace: rows x 2 (the launch lays out the rest)
+    float* parts;                // workspace: parts x 3 x hidden
+    size_t ld_h, ld_d_h, ld_d_z, ld_d_src, ld_d_residual;
+    size_t rows, hidden;
+    size_t part_rows, nparts;
+    uint32_t threshold;
+    float gain, inv_hidden;
+};
+
+struct QuantFp4Args {
+    const void* x;
+    uint8_t* codes;
+    float* scales;
+    size_t ld_x, ld_codes, rows, k;
+    int group;
+};
+
+struct GemmFp4Args {
+    const void* a;
+    const uint8_t* b;
+    const float* b_scales;
+    const int* offsets;          // NULL: one matrix for all rows
+    void* out;
+    size_t ld_a, ld_b, stride_b, ld_out;
+    uint32_t rows, n, k;
+    uint32_t groups;             // of a row of b
+    int experts, group;
+};
+
 // How a kernel spreads `threads` work items (one per 16-byte vector, or 64
 // per wave tile) over the GPU. Decode-size jobs (`small`) get one work item
 // per thread in `wg_small`-thread workgroups, so that even a 512 KiB message
@@ -216,5 +302,15 @@ size_t norm_backward_parts(size_t rows, size_t hidden, size_t gate_rows);
 hipError_t launch_norm_backward(const NormBwdArgs& a, int dtype, hipStream_t s);
 hipError_t launch_quant_i8(const QuantI8Args& a, int dtype, hipStream_t s);
 hipError_t launch_gemm_i8(const GemmI8Args& a, int out_dtype, hipStream_t s);
+
+// Before and behind the experts.
+size_t route_workspace_words(size_t tokens, int experts);
+hipError_t launch_route(const RouteArgs& a, int dtype, hipStream_t s);
+hipError_t launch_route_backward(const RouteBwdArgs& a, int dtype, hipStream_t s);
+hipError_t launch_layer_norm(const LayerNormArgs& a, int dtype, hipStream_t s);
+size_t layer_norm_backward_floats(size_t rows, size_t hidden);
+hipError_t launch_layer_norm_backward(const LayerNormBwdArgs& a, int dtype, hipStream_t s);
+hipError_t launch_quant_fp4(const QuantFp4Args& a, int dtype, hipStream_t s);
+hipError_t launch_gemm_fp4(const GemmFp4Args& a, int dtype, hipStream_t s);
 
 }  // namespace rx

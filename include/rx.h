@@ -509,6 +509,198 @@ rx_status_t rx_gemm_i8(const void* a, size_t ld_a, const float* a_scales,
                        size_t rows, size_t n, size_t k, void* out, size_t ld_out,
                        rx_dtype_t out_dtype, hipStream_t stream);
 
+/*
+ * ---------------------------------------------------------------------------
+ * The router before rx_moe_dispatch, products whose weights have 4 bits, and a
+ * block's end with dropout and layer norm. The conventions of the entry points
+ * above hold: rows `ld` elements apart, pointers aligned to their elements,
+ * 64-bit row offsets, results that do not depend on timing.
+ * ---------------------------------------------------------------------------
+ */
+
+/*
+ * Each token's experts from the router's logits l (tokens x experts), and what
+ * the router is trained with. A token is empty when token_mask is given and its
+ * byte is 0 (its logits are then not used), or when all its logits are -inf.
+ *   P[t, e]        = softmax of row t
+ *   expert_ids[t]  = the topk experts with the largest logits, largest first;
+ *                    of equal ones (-0 equals 0) the lowest number first;
+ *                    -1 for a logit of -inf and for an empty token
+ *   weights[t, j]  = P[t, expert_ids[t, j]], with renormalize divided by the
+ *                    sum of the token's topk; 0 where the id is -1
+ *   lse[t]         = log sum exp of row t; -inf for an empty token
+ *   counts[e]      = pairs with expert e; counts[experts] = n, the tokens that
+ *                    are not empty
+ *   losses[0]      = experts sum over e of f[e] mean of P[t, e] over the n tokens,
+ *                    f[e] = counts[e] / (n topk): 1 for an even load
+ *   losses[1]      = mean of lse[t]^2 over the n tokens
+ * (both 0 when n is 0), in FP32 from the logits on. expert_ids and weights are
+ * what rx_moe_dispatch and rx_moe_combine take. A NaN counts as the largest
+ * logit and makes its token's weights and the losses NaN; the ids stay numbers
+ * of experts.
+ *
+ * logits          : RX_FP32 or RX_BF16.
+ * experts         : 1 .. RX_MAX_EXPERTS; topk: 1 .. the smaller of experts and
+ *                   RX_MAX_TOPK.
+ * token_mask      : NULL, or `tokens` bytes.
+ * expert_ids, weights: tokens x topk, packed.
+ * lse             : NULL, or `tokens` floats; the backward pass needs it.
+ * counts, losses  : both or neither (NULL): experts + 1 integers, 2 floats.
+ * workspace       : rx_moe_route_workspace() bytes, 4-byte aligned, where counts
+ *                   are wanted; its contents on return are unspecified.
+ */
+rx_status_t rx_moe_route(const void* logits, size_t ld_logits,
+                         const unsigned char* token_mask, size_t tokens,
+                         int experts, int topk, int renormalize, rx_dtype_t dtype,
+                         int* expert_ids, float* weights, float* lse, int* counts,
+                         float* losses, void* workspace, size_t workspace_bytes,
+                         hipStream_t stream);
+
+/* Workspace bytes of rx_moe_route; 0 on invalid arguments. Looks up the
+ * device's compute-unit count. */
+size_t rx_moe_route_workspace(size_t tokens, int experts);
+
+/*
+ * Gradient of rx_moe_route with respect to the logits, from d_weights (tokens x
+ * topk) and d_losses (2 values on the device), the gradients of its outputs
+ * (either may be NULL: zero), and the forward call's logits, expert_ids, lse
+ * and counts. The counts are constants, and give both f and n: with counts
+ * that several ranks added up, the losses are those over all their tokens, of
+ * which this call's tokens get their part of the gradient.
+ *   dP[t, e] = d_losses[0] experts f[e] / n  (+ d_weights[t, j] at e =
+ *              expert_ids[t, j], without renormalize)
+ *   dl[t, e] = P (dP - sum over e of P dP) + d_losses[1] 2 lse[t] P / n
+ *              (with renormalize + w_j (d_weights[t, j] - sum over i of w_i
+ *              d_weights[t, i]) at e = expert_ids[t, j])
+ * d_logits = cast(dl), 0 for tokens whose lse is -inf. Ids that are no
+ * expert's number are left out; a token's other ids are distinct.
+ *
+ * counts may be NULL when d_losses is, expert_ids when d_weights is. d_logits:
+ * dtype; may equal logits exactly (same ld).
+ */
+rx_status_t rx_moe_route_backward(const void* logits, size_t ld_logits,
+                                  const int* expert_ids, const float* lse,
+                                  const int* counts, const float* d_weights,
+                                  const float* d_losses, size_t tokens, int experts,
+                                  int topk, int renormalize, rx_dtype_t dtype,
+                                  void* d_logits, size_t ld_d_logits,
+                                  hipStream_t stream);
+
+/*
+ * Rows to 4-bit floating point (OCP E2M1: sign, two exponent bits, one bit of
+ * mantissa; magnitudes 0, 0.5, 1, 1.5, 2, 3, 4, 6) with one FP32 scale for each
+ * group of `group` elements of a row (the row's last group may be shorter):
+ *   A = max |x| over the group, s = A / 6, r = 6 / A (each the correctly
+ *   rounded FP32 quotient; A == 0, s == 0 or r not finite: s = r = 1),
+ *   code = E2M1 nearest to fl32(x r), ties to the even mantissa.
+ * Element 2 i of a row is in the low half of byte i, element 2 i + 1 in the
+ * high half; an odd row's last high half is 0. A group that holds a NaN gets
+ * scale NaN, one that holds an infinity (and no NaN) an infinite scale, both
+ * codes 0: their products are NaN.
+ *
+ * x: RX_FP32 or RX_BF16, rows of k elements; group: 32, 64 or 128; codes:
+ * ld_codes bytes apart, any number from ceil(k / 2) on (rx_gemm_fp4 wants more);
+ * scales: rows x ceil(k / group), packed. k up to 2^23, rows < 2^22.
+ */
+rx_status_t rx_quant_fp4(const void* x, size_t ld_x, size_t rows, size_t k,
+                         rx_dtype_t dtype, int group, void* codes,
+                         size_t ld_codes, float* scales, hipStream_t stream);
+
+/*
+ * Product of rows with weights of 4 bits (rx_quant_fp4's codes and scales, n
+ * rows of k):
+ *   out[m, j] = cast( sum over groups g of b_scales[j, g]
+ *                     sum over i in g of a[m, i] b[j, i] )
+ * The products are exact and the sums in FP32 (a in FP32 is taken apart into
+ * three BF16 parts without loss, but for bits below 2^-133). offsets and experts
+ * as in rx_gemm_i8: b's matrix e starts at b + e stride_b, its scales at
+ * b_scales + e n ceil(k / group), and the rows past offsets[experts] become 0.
+ *
+ * a, out  : dtype (RX_FP32 or RX_BF16).
+ * b       : 16-byte aligned; ld_b (bytes) and stride_b multiples of 16, ld_b at
+ *           least ceil(k / 2) rounded up to 16. The bytes from ceil(k / 2) to that
+ *           multiple are read and may hold anything, as may the high half of an
+ *           odd row's last byte.
+ * group   : 32, 64 or 128. b_scales: FP32, packed.
+ * k       : up to 2^23; k == 0 gives zeros. ld_a and ld_b below 2^23.
+ * rows < 2^22, n < 2^31, and fewer than 2^23 - 16 tiles of 16 x 128 outputs with
+ * a partial one for every expert: (rows / 16 + experts + 1) ceil(n / 128).
+ */
+rx_status_t rx_gemm_fp4(const void* a, size_t ld_a, const void* b, size_t ld_b,
+                        size_t stride_b, const float* b_scales, int group,
+                        const int* offsets, int experts, size_t rows, size_t n,
+                        size_t k, rx_dtype_t dtype, void* out, size_t ld_out,
+                        hipStream_t stream);
+
+/*
+ * A block's end with dropout and layer norm, or each of them alone:
+ *   y = sum of the sources in their order (+ bias), in FP32
+ *   u = y / (1 - p) for the elements that dropout keeps, exactly 0 for the
+ *       others (whatever y is); without dropout u = y
+ *   h = cast( residual + u )                       (residual NULL: cast(u))
+ *   z = cast( (h - mean) rstd w + b ),  rstd = 1 / sqrt(var + eps)
+ * for every row, with the mean and the variance (of all elements, without a
+ * correction) of h as it is stored, in FP32 and the variance about the mean.
+ *
+ * Dropout. p is `drop` rounded to a multiple of 2^-16 (to even); 0 leaves
+ * dropout out. The mask is never stored: it comes from Philox of four words and ten
+ * rounds (Salmon, Moraes, Dror, Shaw: "Parallel random numbers: as easy as 1,
+ * 2, 3", 2011). rng points to two 64-bit numbers on the device, seed and
+ * offset, read when the kernel runs, so that a captured graph can be replayed
+ * with others. Element c of row r takes the 16 bits c % 8 (low halves first) of
+ * the output for the counter (i, offset), i = r ceil(hidden / 8) + c / 8, low
+ * words first, and the key seed, and is dropped when they are below 65536 p.
+ *
+ * srcs, residual: rows of `hidden`, dtype (RX_FP32 or RX_BF16). bias, w, b:
+ *       `hidden` elements of dtype, each may be NULL (0, 1, 0).
+ * out_h, out_z: dtype; either may be NULL. out_h may equal residual or one
+ *       srcs[j] exactly (same ld), and so may out_z when out_h is NULL.
+ * mean, rstd: NULL, or `rows` floats each for the backward pass (only written
+ *       with out_z).
+ * eps: positive and finite. drop: 0 <= p <= 1 - 2^-16. rng: 8-byte aligned,
+ *       may be NULL when p is 0. hidden: up to 32768.
+ * The sum of the squared distances from a row's mean must be an FP32 value:
+ * elements of up to about 1e17 at the largest widths.
+ */
+rx_status_t rx_layer_norm(const void* const* srcs, int nsrc, size_t ld_src,
+                          const void* bias, const void* residual,
+                          size_t ld_residual, const void* w, const void* b,
+                          float eps, float drop, const unsigned long long* rng,
+                          size_t rows, size_t hidden, rx_dtype_t dtype,
+                          void* out_h, size_t ld_h, void* out_z, size_t ld_z,
+                          float* mean, float* rstd, hipStream_t stream);
+
+/*
+ * Gradient of rx_layer_norm from d_h and d_z, the gradients of its two outputs
+ * (either may be NULL: zero), the h it wrote (the source itself where nothing
+ * was added), its mean and rstd, and the same drop and rng. With
+ * x = (h - mean) rstd, a = d_z w and means over the row:
+ *   dH         = d_h + rstd (a - mean(a) - x mean(a x))
+ *   d_residual = cast( dH )
+ *   d_src      = cast( dH / (1 - p) where dropout kept the element, else 0 ):
+ *                the gradient of every one of the sources
+ *   d_bias     = sum over rows of that, before the cast
+ *   d_w, d_b   = sums over rows of d_z x and of d_z
+ * h, d_h, d_z, d_src, d_residual: dtype, rows of `hidden`. d_src and d_residual:
+ * each may be NULL, and may equal d_h or d_z exactly (same ld), not each other.
+ * d_bias, d_w, d_b: FP32, packed, each may be NULL. h, mean and rstd may be
+ * NULL when d_z is; d_w and d_b then become 0.
+ * workspace: rx_layer_norm_backward_workspace() bytes, 16-byte aligned.
+ */
+rx_status_t rx_layer_norm_backward(const void* h, size_t ld_h, const void* w,
+                                   const float* mean, const float* rstd, float drop,
+                                   const unsigned long long* rng, size_t rows,
+                                   size_t hidden, rx_dtype_t dtype, const void* d_h,
+                                   size_t ld_d_h, const void* d_z, size_t ld_d_z,
+                                   void* d_src, size_t ld_d_src, void* d_residual,
+                                   size_t ld_d_residual, float* d_bias, float* d_w,
+                                   float* d_b, void* workspace,
+                                   size_t workspace_bytes, hipStream_t stream);
+
+/* Workspace bytes of rx_layer_norm_backward for any of its optional operands;
+ * 0 on invalid arguments. Looks up the device's compute-unit count. */
+size_t rx_layer_norm_backward_workspace(size_t rows, size_t hidden);
+
 /* Static description of a status code (never NULL). */
 const char* rx_status_string(rx_status_t s);
 

@@ -416,10 +416,12 @@ def _bind():
         spec = importlib.util.spec_from_file_location("_rxbind", path)
         m = importlib.util.module_from_spec(spec)
         spec.loader.exec_module(m)
-        m.connect(torch._C._cuda_getCurrentRawStream, *(ctypes.cast(fn, ctypes.c_void_p).value for fn in (
+        at = lambda *fns: [ctypes.cast(fn, ctypes.c_void_p).value for fn in fns]
+        m.connect(torch._C._cuda_getCurrentRawStream, *at(
             L.rx_moe_dispatch, L.rx_moe_combine, L.rx_moe_combine_backward, L.rx_residual_norm,
-            L.rx_residual_norm_backward, L.rx_quant_i8, L.rx_gemm_i8, L.rx_moe_route, L.rx_moe_route_backward,
-            L.rx_quant_fp4, L.rx_gemm_fp4, L.rx_layer_norm, L.rx_layer_norm_backward)))
+            L.rx_residual_norm_backward, L.rx_quant_i8, L.rx_gemm_i8))
+        m.connect_layers(*at(L.rx_moe_route, L.rx_moe_route_backward, L.rx_quant_fp4, L.rx_gemm_fp4,
+                             L.rx_layer_norm, L.rx_layer_norm_backward))
         _bound = m
     return _bound
 

@@ -25,14 +25,19 @@ struct {
     decltype(&rx_residual_norm_backward) residual_norm_backward;
     decltype(&rx_quant_i8) quant_i8;
     decltype(&rx_gemm_i8) gemm_i8;
+} rx;
+constexpr int kEntries = sizeof(rx) / sizeof(void*);
+
+// ... and of the router, the 4-bit weights and the layer norm (connect_layers()).
+struct {
     decltype(&rx_moe_route) moe_route;
     decltype(&rx_moe_route_backward) moe_route_backward;
     decltype(&rx_quant_fp4) quant_fp4;
     decltype(&rx_gemm_fp4) gemm_fp4;
     decltype(&rx_layer_norm) layer_norm;
     decltype(&rx_layer_norm_backward) layer_norm_backward;
-} rx;
-constexpr int kEntries = sizeof(rx) / sizeof(void*);
+} layers;
+constexpr int kLayerEntries = sizeof(layers) / sizeof(void*);
 
 template <class... A>
 [[noreturn]] void refuse(PyObject* type, const char* format, A... a)
@@ -503,7 +508,7 @@ int moe_route(PyObject* const* a, Py_ssize_t n)
     void* ws = workspace(w.dev, a[10], &bytes);
     const hipStream_t stream = w.stream();
     NoGil open;
-    return rx.moe_route(logits.data_ptr(), ld, mask, tokens, (int)experts, (int)topk, renormalize, dt, pi, pw, lse, counts, losses,
+    return layers.moe_route(logits.data_ptr(), ld, mask, tokens, (int)experts, (int)topk, renormalize, dt, pi, pw, lse, counts, losses,
                         ws, bytes, stream);
 }
 
@@ -527,7 +532,7 @@ int moe_route_backward(PyObject* const* a, Py_ssize_t n)
     const bool renormalize = truth(a[9]);
     const hipStream_t stream = w.stream();
     NoGil open;
-    return rx.moe_route_backward(logits.data_ptr(), ld, pi, lse, counts, dw, dl, tokens, (int)experts, (int)topk, renormalize, dt,
+    return layers.moe_route_backward(logits.data_ptr(), ld, pi, lse, counts, dw, dl, tokens, (int)experts, (int)topk, renormalize, dt,
                                  d.data_ptr(), ld_d, stream);
 }
 
@@ -551,7 +556,7 @@ int quant_fp4(PyObject* const* a, Py_ssize_t n)
     float* ps = (float*)packed(w.dev, at::kFloat, {rows, groups_of(k, group)}, "scales", scales);
     const hipStream_t stream = w.stream();
     NoGil open;
-    return rx.quant_fp4(x.data_ptr(), ld_x, rows, k, dt, group, codes.data_ptr(), ld_c, ps, stream);
+    return layers.quant_fp4(x.data_ptr(), ld_x, rows, k, dt, group, codes.data_ptr(), ld_c, ps, stream);
 }
 
 int gemm_fp4(PyObject* const* a, Py_ssize_t n)
@@ -587,7 +592,7 @@ int gemm_fp4(PyObject* const* a, Py_ssize_t n)
     check_padded(tb, half, "b");
     const hipStream_t stream = w.stream();
     NoGil open;
-    return rx.gemm_fp4(ta.data_ptr(), ld_a, tb.data_ptr(), ld_b, stride_b, sb, group, offsets, (int)experts, rows, cols, k, dt,
+    return layers.gemm_fp4(ta.data_ptr(), ld_a, tb.data_ptr(), ld_b, stride_b, sb, group, offsets, (int)experts, rows, cols, k, dt,
                        out.data_ptr(), ld_o, stream);
 }
 
@@ -624,7 +629,7 @@ int layer_norm(PyObject* const* a, Py_ssize_t n)
     const unsigned long long* rng = generator(w.dev, a[12]);
     const hipStream_t stream = w.stream();
     NoGil open;
-    return rx.layer_norm(in.src, in.nsrc, in.ld_src, bias, in.residual, in.ld_residual, pw, pb, eps, drop, rng, in.rows, in.hidden,
+    return layers.layer_norm(in.src, in.nsrc, in.ld_src, bias, in.residual, in.ld_residual, pw, pb, eps, drop, rng, in.rows, in.hidden,
                          in.dtype, h, ld_h, z, ld_z, mean, rstd, stream);
 }
 
@@ -662,8 +667,16 @@ int layer_norm_backward(PyObject* const* a, Py_ssize_t n)
     void* ws = workspace(w.dev, a[15], &bytes);
     const hipStream_t stream = w.stream();
     NoGil open;
-    return rx.layer_norm_backward(m[0], ld[0], pw, mean, rstd, drop, rng, rows, hidden, dt, m[1], ld[1], m[2], ld[2], m[3], ld[3],
+    return layers.layer_norm_backward(m[0], ld[0], pw, mean, rstd, drop, rng, rows, hidden, dt, m[1], ld[1], m[2], ld[2], m[3], ld[3],
                                   m[4], ld[4], d_bias, d_w, d_b, ws, bytes, stream);
+}
+
+// A table's entry points from their addresses, in its order.
+void fill(void* table, PyObject* const* a, int n)
+{
+    void** to = static_cast<void**>(table);
+    for (int i = 0; i < n; ++i)
+        to[i] = reinterpret_cast<void*>((intptr_t)integer(a[i]));
 }
 
 // connect(torch's stream lookup, addresses of the entry points in the order
@@ -674,9 +687,16 @@ int connect(PyObject* const* a, Py_ssize_t n)
         refuse(PyExc_TypeError, "a function and %d addresses", kEntries);
     Py_INCREF(a[0]);
     current_stream = a[0];
-    void** to = reinterpret_cast<void**>(&rx);
-    for (int i = 0; i < kEntries; ++i)
-        to[i] = reinterpret_cast<void*>((intptr_t)integer(a[i + 1]));
+    fill(&rx, a + 1, kEntries);
+    return 0;
+}
+
+// connect_layers(addresses of the entry points in the order of `layers`)
+int connect_layers(PyObject* const* a, Py_ssize_t n)
+{
+    if (n != kLayerEntries)
+        refuse(PyExc_TypeError, "%d addresses", kLayerEntries);
+    fill(&layers, a, kLayerEntries);
     return 0;
 }
 
@@ -695,7 +715,7 @@ PyObject* entry(PyObject*, PyObject* const* a, Py_ssize_t n)
 
 #define RX_ENTRY(NAME) {#NAME, (PyCFunction)(void*)entry<NAME>, METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {
-    RX_ENTRY(connect), RX_ENTRY(moe_dispatch), RX_ENTRY(moe_combine), RX_ENTRY(moe_combine_backward),
+    RX_ENTRY(connect), RX_ENTRY(connect_layers), RX_ENTRY(moe_dispatch), RX_ENTRY(moe_combine), RX_ENTRY(moe_combine_backward),
     RX_ENTRY(residual_norm), RX_ENTRY(residual_norm_backward), RX_ENTRY(quant_i8), RX_ENTRY(gemm_i8),
     RX_ENTRY(moe_route), RX_ENTRY(moe_route_backward), RX_ENTRY(quant_fp4), RX_ENTRY(gemm_fp4), RX_ENTRY(layer_norm),
     RX_ENTRY(layer_norm_backward),

@@ -312,5 +312,12 @@ size_t layer_norm_backward_floats(size_t rows, size_t hidden);
 hipError_t launch_layer_norm_backward(const LayerNormBwdArgs& a, int dtype, hipStream_t s);
 hipError_t launch_quant_fp4(const QuantFp4Args& a, int dtype, hipStream_t s);
 hipError_t launch_gemm_fp4(const GemmFp4Args& a, int dtype, hipStream_t s);
+// ... by type and group size
+hipError_t launch_fp4_fp32_32(const GemmFp4Args& a, hipStream_t s);
+hipError_t launch_fp4_fp32_64(const GemmFp4Args& a, hipStream_t s);
+hipError_t launch_fp4_fp32_128(const GemmFp4Args& a, hipStream_t s);
+hipError_t launch_fp4_bf16_32(const GemmFp4Args& a, hipStream_t s);
+hipError_t launch_fp4_bf16_64(const GemmFp4Args& a, hipStream_t s);
+hipError_t launch_fp4_bf16_128(const GemmFp4Args& a, hipStream_t s);
 
 }  // namespace rx

@@ -264,10 +264,13 @@ def test_gemm_fp4_dense(dtype, m, n, k, group):
 
 @pytest.mark.parametrize("dtype", DTYPES)
 @pytest.mark.parametrize("group", [32, 128])
-@pytest.mark.parametrize("m,n,k", [(1, 4100, 300), (20, 4100, 300), (40, 4100, 300), (70, 9000, 130), (500, 1100, 300), (1024, 600, 300)])
-def test_gemm_fp4_tiles(dtype, group, m, n, k):
-    """Sizes of every tile."""
-    check_gemm(dtype, m, n, k, group)
+@pytest.mark.parametrize("m,n,k", [
+    (1, 2000, 1304), (3, 5000, 2056), (13, 2000, 1304), (16, 5000, 2056), (16, 40000, 520), (20, 3000, 1304), (30, 5000, 1304), (30, 40000, 264),
+    (60, 5000, 776), (61, 40000, 264), (600, 5000, 392), (1200, 9000, 136), (2000, 9000, 264)])
+@pytest.mark.parametrize("odd", [0, 3])
+def test_gemm_fp4_tiles(dtype, group, m, n, k, odd):
+    """Sizes of every tile; rows of whole 16-byte units, and others."""
+    check_gemm(dtype, m, n, k - odd, group)
 
 
 @pytest.mark.parametrize("dtype", DTYPES)

@@ -11,7 +11,6 @@
 namespace rx {
 namespace {
 
-constexpr int kRouteWaves = 4;
 
 template <int G>
 __device__ __forceinline__ float group_sum(float v)
@@ -32,123 +31,212 @@ __device__ __forceinline__ float group_sum(float v)
     return v;
 }
 
-// Logits pos V .. pos V + V - 1 of a row.
+// Logits pos V .. pos V + V - 1 of a row: the loads, which wait for nothing, and
+// their values.
+template <int DT, int V> struct RawLogits { u32x4 v[V / Elem<DT>::kVE]; };
+
 template <int DT, int V>
-__device__ __forceinline__ void ld_logits(const void* row, int pos, int experts, float* x)
+__device__ __forceinline__ RawLogits<DT, V> ld_logits(const void* row, int pos, int experts)
 {
-    constexpr int VE = Elem<DT>::kVE;
-    u32x4 r[V / VE];
+    constexpr int N = V / Elem<DT>::kVE;
+    RawLogits<DT, V> r;
 #pragma unroll
-    for (int i = 0; i < V / VE; ++i)
-        r[i] = ld_raw<DT, true>(row, pos * (V / VE) + i, experts);
+    for (int i = 0; i < N; ++i)
+        r.v[i] = ld_raw<DT, true>(row, pos * N + i, experts);
+    return r;
+}
+template <int DT, int V>
+__device__ __forceinline__ void logits_of(const RawLogits<DT, V>& r, int pos, int experts, float* x)
+{
+    constexpr int VE = Elem<DT>::kVE, N = V / VE;
 #pragma unroll
-    for (int i = 0; i < V / VE; ++i)
-        unpack<DT>(fixed<DT, true>(r[i], pos * (V / VE) + i, experts), x + i * VE);
+    for (int i = 0; i < N; ++i)
+        unpack<DT>(fixed<DT, true>(r.v[i], pos * N + i, experts), x + i * VE);
 }
 
-// Unsigned numbers in the logits' order: -inf is kKeyNone, what is taken or
-// past the experts 0, NaN above all; -0 equals 0.
+// Unsigned numbers in the logits' order, the lower expert's above its equal's: what
+// is taken or past the experts is 0, -inf at most kKeyNone, NaN above all; -0
+// equals 0. A BF16 logit leaves 16 bits for its expert, so that one comparison
+// finds the largest and its place.
 constexpr uint32_t kKeyNone = 0x007FFFFFu;
-__device__ __forceinline__ uint32_t key_of(float x)
+template <int DT>
+__device__ __forceinline__ uint32_t key_of(float x, int expert)
 {
     uint32_t u = __builtin_bit_cast(uint32_t, x + 0.0f);
     u = x != x ? 0x7FC00000u : u;
-    return u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
+    u ^= (uint32_t)((int32_t)u >> 31) | 0x80000000u;
+    return DT == 0 ? u : (u & 0xFFFF0000u) | (0xFFFFu - (uint32_t)expert);
 }
+template <int DT>
 __device__ __forceinline__ float value_of(uint32_t key)
 {
-    return bits_f32(key ^ (key >> 31 ? 0x80000000u : 0xFFFFFFFFu));
+    const uint32_t u = key ^ (key >> 31 ? 0x80000000u : 0xFFFFFFFFu);
+    return bits_f32(DT == 0 ? u : u & 0xFFFF0000u);
 }
 
-// What a workgroup leaves for the second launch: experts counts, experts sums
-// of P, its tokens and the sum of their lse^2.
-__device__ __forceinline__ uint32_t part_words(int experts) { return 2 * (uint32_t)experts + 2; }
+// The workspace: a counter; for each workgroup a part (experts counts, experts
+// sums of P), then for each its tokens and the sum of their lse^2; and a sum for
+// each workgroup of the second launch.
+__device__ __host__ __forceinline__ size_t part_words(int experts) { return 2 * (size_t)experts; }
+constexpr int kSumExperts = 32;   // of a workgroup of the second launch
+
+// Sum over the lanes at this one's place in each group of G, the same in all.
+template <int G>
+__device__ __forceinline__ float across(float v)
+{
+    auto u = [](float x) { return __builtin_bit_cast(uint32_t, x); };
+    if constexpr (G <= 1) v += bits_f32(dpp<0x121>(u(v)));   // row_ror 1, 2, 4, 8
+    if constexpr (G <= 2) v += bits_f32(dpp<0x122>(u(v)));
+    if constexpr (G <= 4) v += bits_f32(dpp<0x124>(u(v)));
+    if constexpr (G <= 8) v += bits_f32(dpp<0x128>(u(v)));
+    if constexpr (G <= 16) {
+        auto p = __builtin_amdgcn_permlane16_swap(u(v), u(v), false, false);
+        v = bits_f32(p[0]) + bits_f32(p[1]);
+    }
+    if constexpr (G <= 32) {
+        auto p = __builtin_amdgcn_permlane32_swap(u(v), u(v), false, false);
+        v = bits_f32(p[0]) + bits_f32(p[1]);
+    }
+    return v;
+}
+template <int G>
+__device__ __forceinline__ uint32_t across(uint32_t v)
+{
+    if constexpr (G <= 1) v += dpp<0x121>(v);
+    if constexpr (G <= 2) v += dpp<0x122>(v);
+    if constexpr (G <= 4) v += dpp<0x124>(v);
+    if constexpr (G <= 8) v += dpp<0x128>(v);
+    if constexpr (G <= 16) {
+        auto p = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+        v = p[0] + p[1];
+    }
+    if constexpr (G <= 32) {
+        auto p = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+        v = p[0] + p[1];
+    }
+    return v;
+}
+
+// The losses from n tokens, the sum over the experts of count times sum of P,
+// and the sum of lse^2.
+__device__ __forceinline__ void put_losses(const RouteArgs& a, uint32_t n, float dot, float z)
+{
+    const float inv = n ? 1.0f / (float)n : 0.0f;
+    a.counts[a.experts] = (int)n;
+    a.losses[0] = dot * inv * inv * ((float)a.experts / (float)a.topk);
+    a.losses[1] = z * inv;
+}
+
+template <int V> constexpr int kRouteWaves = V == 16 ? 8 : 16;   // at most: what the registers allow
 
 template <int DT, int G, int V, bool SUMS>
-__global__ __launch_bounds__(kRouteWaves * kWave) void k_route(RouteArgs a)
+__global__ __launch_bounds__(kRouteWaves<V> * kWave) void k_route(RouteArgs a)
 {
     constexpr int TW = kWave / G;                                // tokens of a wave
     constexpr int MOST = V * G < kMaxTopk ? V * G : kMaxTopk;    // choices of a token
+    constexpr int W = kRouteWaves<V>;
     struct Pick {
         int id;
-        float e;
+        uint32_t key;
     };
-    __shared__ Pick picks[kRouteWaves][TW * MOST];
-    __shared__ uint32_t sums[SUMS ? kRouteWaves : 1][SUMS ? V * G : 1];
-    __shared__ uint32_t totals[kRouteWaves][2];
-    const int lane = lane_id(), wave = threadIdx.x / kWave, pos = lane % G, sub = lane / G;
+    __shared__ Pick picks[W][TW * MOST];
+    __shared__ uint32_t sums[SUMS ? 2 : 1][SUMS ? W : 1][SUMS ? V * G : 1];
+    __shared__ uint32_t totals[W][2];
+    __shared__ float dots[W];
+    const int lane = lane_id(), wave = threadIdx.x / kWave, waves = blockDim.x / kWave, pos = lane % G, sub = lane / G;
     const int experts = a.experts, topk = a.topk;
     float prob[V] = {}, squares = 0.0f;
     uint32_t count[V] = {}, live_tokens = 0;
-    const size_t step = (size_t)gridDim.x * kRouteWaves * TW;
-    for (size_t t0 = ((size_t)blockIdx.x * kRouteWaves + wave) * TW; t0 < a.tokens; t0 += step) {
+    const size_t step = (size_t)gridDim.x * waves * TW;
+    for (size_t t0 = ((size_t)blockIdx.x * waves + wave) * TW; t0 < a.tokens; t0 += step) {
         const size_t t = t0 + sub;
+        // an empty token's logits are loaded too: no wait for the mask
+        const RawLogits<DT, V> raw =
+            ld_logits<DT, V>(static_cast<const char*>(a.logits) + (t < a.tokens ? t : a.tokens - 1) * a.ld * Elem<DT>::kBytes, pos, experts);
         bool live = t < a.tokens && (!a.mask || a.mask[t]);
         float x[V];
         uint32_t key[V];
-        if (live)
-            ld_logits<DT, V>(static_cast<const char*>(a.logits) + t * a.ld * Elem<DT>::kBytes, pos, experts, x);
-#pragma unroll
-        for (int i = 0; i < V; ++i)
-            key[i] = live && pos * V + i < experts ? key_of(x[i]) : 0;
+        logits_of<DT, V>(raw, pos, experts, x);
         uint32_t mine = 0;
 #pragma unroll
-        for (int i = 0; i < V; ++i)
+        for (int i = 0; i < V; ++i) {
+            key[i] = live && pos * V + i < experts ? key_of<DT>(x[i], pos * V + i) : 0;
             mine = umax(mine, key[i]);
+        }
         uint32_t top = group_max<G>(mine);
         live = top > kKeyNone;
-        const float high = live ? value_of(top) : 0.0f;
+        const float high = live ? value_of<DT>(top) : 0.0f;
         float sum = 0.0f, e[V];
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            e[i] = live && pos * V + i < experts ? expf(x[i] - high) : 0.0f;
+            e[i] = expf(key[i] ? x[i] - high : -__builtin_inff());   // 0 for an empty token
             sum += e[i];
         }
         sum = group_sum<G>(sum);
-        // the choices, one a round
+        // the choices, one a round; what is taken has no key any more
         Pick* pick = picks[wave] + sub * topk;
-        float chosen = 0.0f;
-        uint32_t taken = 0;
+        uint32_t kept = 0;   // logits that can be taken
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            kept |= key[i] > kKeyNone ? 1u << i : 0;
         for (int j = 0; j < topk; ++j) {
-            const uint64_t owners = __ballot(mine == top) >> (sub * G);
-            const bool any = top > kKeyNone, owner = any && pos == __builtin_ctzll(owners);
-            const float w = any ? expf(value_of(top) - high) : 0.0f;
-            chosen += w;
-            if (owner) {
-                uint32_t first = 0;
+            if constexpr (DT == 0) {
+                const uint64_t owners = __ballot(mine == top) >> (sub * G);
+                bool mayhave = pos == __builtin_ctzll(owners);
+                int id = -1;
 #pragma unroll
-                for (int i = V - 1; i >= 0; --i)
-                    first = key[i] == top ? (uint32_t)i : first;
+                for (int i = 0; i < V; ++i) {
+                    const bool hit = mayhave && key[i] == top;   // the first of equals
+                    mayhave = mayhave && !hit;
+                    id = hit ? i : id;
+                    key[i] = hit ? 0 : key[i];
+                }
+                if (id >= 0)
+                    pick[j] = Pick{pos * V + id, top};
+            } else {
+                if (pos == 0)
+                    pick[j] = Pick{(int)(0xFFFFu - (top & 0xFFFFu)), top};
 #pragma unroll
                 for (int i = 0; i < V; ++i)
-                    key[i] = (uint32_t)i == first ? 0 : key[i];
-                taken |= 1u << first;
-                pick[j] = Pick{pos * V + (int)first, w};
-                mine = 0;
-#pragma unroll
-                for (int i = 0; i < V; ++i)
-                    mine = umax(mine, key[i]);
+                    key[i] = key[i] == top ? 0 : key[i];
             }
-            if (!any && pos == 0)
-                pick[j] = Pick{-1, 0.0f};
+            mine = 0;
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+                mine = umax(mine, key[i]);
             top = group_max<G>(mine);
         }
-        const float by = a.renormalize ? chosen : sum;
-        const float scale = live ? by : 1.0f;
+        uint32_t taken = 0;
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            taken |= key[i] == 0 ? kept & 1u << i : 0;
+        float chosen = sum;
+        if (a.renormalize) {
+            chosen = 0.0f;
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+                chosen += taken >> i & 1 ? e[i] : 0.0f;
+            chosen = group_sum<G>(chosen);
+        }
+        const float scale = live ? chosen : 1.0f;
+        const float lse = live ? high + logf(sum) : -__builtin_inff();
         if (a.lse && pos == 0 && t < a.tokens)
-            a.lse[t] = live ? high + logf(sum) : -__builtin_inff();
+            a.lse[t] = lse;
         // tokens of the wave follow each other: their choices too
         const size_t left = a.tokens - t0;
         const int n = (left < (size_t)TW ? (int)left : TW) * topk;
         wave_sync();
         for (int i0 = 0; i0 < n; i0 += kWave) {
             const int i = i0 + lane;
-            // the divisor of the token that choice i belongs to
-            const float div = bits_f32((uint32_t)__builtin_amdgcn_ds_bpermute((i < n ? i / topk : 0) * G * 4, (int)__builtin_bit_cast(uint32_t, scale)));
+            // the largest logit and the divisor of the token that choice i belongs to
+            const int from = (i < n ? i / topk : 0) * G * 4;
+            const float top_of = bits_f32((uint32_t)__builtin_amdgcn_ds_bpermute(from, (int)__builtin_bit_cast(uint32_t, high)));
+            const float div = bits_f32((uint32_t)__builtin_amdgcn_ds_bpermute(from, (int)__builtin_bit_cast(uint32_t, scale)));
             if (i < n) {
                 const Pick p = picks[wave][i];
-                a.ids[t0 * topk + i] = p.id;
-                a.weights[t0 * topk + i] = p.e / div;
+                const bool some = p.key > kKeyNone;
+                a.ids[t0 * topk + i] = some ? p.id : -1;
+                a.weights[t0 * topk + i] = some ? expf(value_of<DT>(p.key) - top_of) / div : 0.0f;
             }
         }
         wave_sync();
@@ -160,44 +248,24 @@ __global__ __launch_bounds__(kRouteWaves * kWave) void k_route(RouteArgs a)
                 count[i] += taken >> i & 1;
             }
             if (live && pos == 0) {
-                const float l = high + logf(sum);
-                squares += l * l;
+                squares += lse * lse;
                 ++live_tokens;
             }
         }
     }
     if constexpr (SUMS) {
         // over the wave's groups, then over the waves, in their order
-        uint32_t* out = a.workspace + 1 + (size_t)blockIdx.x * part_words(experts);
-        auto across = [&](float v) {
-            for (int d = G; d < kWave; d *= 2)
-                v += bits_f32((uint32_t)__builtin_amdgcn_ds_bpermute((lane ^ d) * 4, (int)__builtin_bit_cast(uint32_t, v)));
-            return v;
-        };
-        auto across_u = [&](uint32_t v) {
-            for (int d = G; d < kWave; d *= 2)
-                v += (uint32_t)__builtin_amdgcn_ds_bpermute((lane ^ d) * 4, (int)v);
-            return v;
-        };
+        const bool alone = gridDim.x == 1;
+        uint32_t* out = a.workspace + 1 + blockIdx.x * part_words(experts);
+        if (blockIdx.x == 0 && threadIdx.x == 0)
+            a.workspace[0] = 0;   // the second launch's counter
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            const uint32_t c = across_u(count[i]);
-            if (sub == 0)
-                sums[wave][pos * V + i] = c;
-        }
-        __syncthreads();
-        for (int e = threadIdx.x; e < experts; e += kRouteWaves * kWave) {
-            uint32_t c = 0;
-            for (int w = 0; w < kRouteWaves; ++w)
-                c += sums[w][e];
-            out[e] = c;
-        }
-        __syncthreads();
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-            const float p = across(prob[i]);
-            if (sub == 0)
-                sums[wave][pos * V + i] = __builtin_bit_cast(uint32_t, p);
+            const uint32_t c = across<G>(count[i]), p = __builtin_bit_cast(uint32_t, across<G>(prob[i]));
+            if (sub == 0) {
+                sums[0][wave][pos * V + i] = c;
+                sums[1][wave][pos * V + i] = p;
+            }
         }
         squares = wave_sum(squares);
         live_tokens = wave_sum_u(live_tokens);
@@ -206,73 +274,117 @@ __global__ __launch_bounds__(kRouteWaves * kWave) void k_route(RouteArgs a)
             totals[wave][1] = __builtin_bit_cast(uint32_t, squares);
         }
         __syncthreads();
-        for (int e = threadIdx.x; e < experts; e += kRouteWaves * kWave) {
+        float dot = 0.0f;
+        for (int e = threadIdx.x; e < experts; e += blockDim.x) {
+            uint32_t c = 0;
             float p = 0.0f;
-            for (int w = 0; w < kRouteWaves; ++w)
-                p += bits_f32(sums[w][e]);
-            out[experts + e] = __builtin_bit_cast(uint32_t, p);
+            for (int w = 0; w < waves; ++w) {
+                c += sums[0][w][e];
+                p += bits_f32(sums[1][w][e]);
+            }
+            dot += (float)c * p;
+            if (alone) {
+                a.counts[e] = (int)c;
+            } else {
+                out[e] = c;
+                out[experts + e] = __builtin_bit_cast(uint32_t, p);
+            }
+        }
+        if (alone) {
+            dot = wave_sum(dot);
+            if (lane == 0)
+                dots[wave] = dot;
+            __syncthreads();
         }
         if (threadIdx.x == 0) {
             uint32_t n = 0;
-            float z = 0.0f;
-            for (int w = 0; w < kRouteWaves; ++w) {
+            float z = 0.0f, d = 0.0f;
+            for (int w = 0; w < waves; ++w) {
                 n += totals[w][0];
                 z += bits_f32(totals[w][1]);
+                d += alone ? dots[w] : 0.0f;
             }
-            out[2 * experts] = n;
-            out[2 * experts + 1] = __builtin_bit_cast(uint32_t, z);
+            if (alone) {
+                put_losses(a, n, d, z);
+            } else {
+                out = a.workspace + 1 + a.parts * part_words(experts) + 2 * blockIdx.x;
+                out[0] = n;
+                out[1] = __builtin_bit_cast(uint32_t, z);
+            }
         }
     }
 }
 
-// The workgroups' sums in their order, and the losses: one workgroup.
+// The workgroups' parts in their order: 32 experts a workgroup, half the lanes for
+// the counts and half for the sums of P, the parts dealt to 16 waves, 16 of a
+// wave's loads at a time. The last workgroup to come adds the workgroups' share of
+// the loss.
 __global__ __launch_bounds__(1024) void k_route_sums(RouteArgs a)
 {
-    __shared__ float lds[16];
-    __shared__ uint32_t lds_n[16];
-    __shared__ float lds_z[16];
+    __shared__ uint32_t sums[16][kWave], n_of[16], order;
+    __shared__ float z_of[16];
     const int experts = a.experts, lane = lane_id(), wave = threadIdx.x / kWave;
-    const uint32_t* in = a.workspace + 1;
+    const int e = (int)blockIdx.x * kSumExperts + lane % kSumExperts;
+    const bool counts = lane < kSumExperts;
     const size_t words = part_words(experts);
-    float dot = 0.0f;
-    for (int e = threadIdx.x; e < experts; e += 1024) {
-        uint32_t c = 0;
-        float p = 0.0f;
-        for (uint32_t g = 0; g < a.parts; ++g) {
-            c += in[g * words + e];
-            p += bits_f32(in[g * words + experts + e]);
+    const uint32_t *in = a.workspace + 1, *totals = in + a.parts * words;
+    float* shares = reinterpret_cast<float*>(a.workspace + 1 + a.parts * (words + 2));
+    const uint32_t* at = in + (counts ? 0 : experts) + (e < experts ? e : 0);
+    uint32_t n = 0, c = 0;
+    float z = 0.0f, p = 0.0f;
+    if (threadIdx.x < a.parts) {   // at most 1024
+        n = totals[2 * threadIdx.x];
+        z = bits_f32(totals[2 * threadIdx.x + 1]);
+    }
+    for (uint32_t g0 = wave; g0 < a.parts; g0 += 256) {
+        uint32_t x[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            const uint32_t g = g0 + 16 * i;
+            x[i] = at[(g < a.parts ? g : g0) * words];
         }
-        a.counts[e] = (int)c;
-        dot += (float)c * p;
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+            if (g0 + 16 * i < a.parts) {
+                c += x[i];
+                p += bits_f32(x[i]);
+            }
     }
-    uint32_t n = 0;
-    float z = 0.0f;
-    for (uint32_t g = threadIdx.x; g < a.parts; g += 1024) {
-        n += in[g * words + 2 * experts];
-        z += bits_f32(in[g * words + 2 * experts + 1]);
-    }
+    sums[wave][lane] = counts ? c : __builtin_bit_cast(uint32_t, p);
     n = wave_sum_u(n);
     z = wave_sum(z);
-    dot = wave_sum(dot);
     if (lane == 0) {
-        lds[wave] = dot;
-        lds_n[wave] = n;
-        lds_z[wave] = z;
+        n_of[wave] = n;
+        z_of[wave] = z;
     }
     __syncthreads();
-    if (threadIdx.x)
+    if (wave)
         return;
-    dot = z = 0.0f;
-    n = 0;
+    c = n = 0;
+    p = z = 0.0f;
+#pragma unroll
     for (int w = 0; w < 16; ++w) {
-        dot += lds[w];
-        n += lds_n[w];
-        z += lds_z[w];
+        c += sums[w][lane % kSumExperts];
+        p += bits_f32(sums[w][kSumExperts + lane % kSumExperts]);
+        n += n_of[w];
+        z += z_of[w];
     }
-    a.counts[experts] = (int)n;
-    const float inv = n ? 1.0f / (float)n : 0.0f;
-    a.losses[0] = dot * inv * inv * ((float)experts / (float)a.topk);
-    a.losses[1] = z * inv;
+    if (counts && e < experts)
+        a.counts[e] = (int)c;
+    float dot = wave_sum(counts && e < experts ? (float)c * p : 0.0f);
+    if (gridDim.x > 1) {
+        if (lane == 0) {
+            __hip_atomic_store(&shares[blockIdx.x], dot, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            order = __hip_atomic_fetch_add(&a.workspace[0], 1u, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT);
+        }
+        wave_sync();
+        if (order != gridDim.x - 1)
+            return;
+        // at most 32 shares, a lane each
+        dot = wave_sum((uint32_t)lane < gridDim.x ? __hip_atomic_load(&shares[lane], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) : 0.0f);
+    }
+    if (lane == 0)
+        put_losses(a, n, dot, z);
 }
 
 // ---- gradient ------------------------------------------------------------------
@@ -280,43 +392,56 @@ __global__ __launch_bounds__(1024) void k_route_sums(RouteArgs a)
 // dl = P (c f + h - A + z), with c f from the counts, h and A from the weights'
 // gradients: an element of the token's choices in LDS at a time.
 template <int DT, int G, int V>
-__global__ __launch_bounds__(kRouteWaves * kWave) void k_route_backward(RouteBwdArgs a)
+__global__ __launch_bounds__(256) void k_route_backward(RouteBwdArgs a)
 {
-    constexpr int TW = kWave / G, VE = Elem<DT>::kVE;
+    constexpr int TW = kWave / G, VE = Elem<DT>::kVE, kWaves = 4;
     constexpr uint32_t kNone = 0x7FFFDEADu;   // no choice: a NaN that no gradient has
-    __shared__ uint32_t grads[kRouteWaves][TW * G * V];
+    __shared__ uint32_t grads[kWaves][TW * G * V];
     const int lane = lane_id(), wave = threadIdx.x / kWave, pos = lane % G, sub = lane / G;
     const int experts = a.experts, topk = a.topk;
     float load[V] = {}, zc = 0.0f;
-    if (a.d_losses) {
-        const int n = a.counts[experts];
-        const float inv = n > 0 ? 1.0f / (float)n : 0.0f;
-        const float c = a.d_losses[0] * ((float)experts / (float)topk) * inv * inv;
-        zc = 2.0f * a.d_losses[1] * inv;
-#pragma unroll
-        for (int i = 0; i < V; ++i)
-            load[i] = pos * V + i < experts ? c * (float)a.counts[pos * V + i] : 0.0f;
-    }
     uint32_t* grad = grads[wave];
-    const size_t step = (size_t)gridDim.x * kRouteWaves * TW;
-    for (size_t t0 = ((size_t)blockIdx.x * kRouteWaves + wave) * TW; t0 < a.tokens; t0 += step) {
-        const size_t t = t0 + sub;
-        const float lse = t < a.tokens ? a.lse[t] : -__builtin_inff();
+    const size_t step = (size_t)gridDim.x * kWaves * TW;
+    bool first = true;
+    for (size_t t0 = ((size_t)blockIdx.x * kWaves + wave) * TW; t0 < a.tokens; t0 += step) {
+        // all loads before anything waits
+        const size_t t = t0 + sub, row = t < a.tokens ? t : a.tokens - 1;
+        const RawLogits<DT, V> raw = ld_logits<DT, V>(static_cast<const char*>(a.logits) + row * a.ld * Elem<DT>::kBytes, pos, experts);
+        const float lse = t < a.tokens ? a.lse[row] : -__builtin_inff();
+        const size_t left = a.tokens - t0;
+        const int n = (left < (size_t)TW ? (int)left : TW) * topk;
+        int id = -1;
+        float dw = 0.0f;
+        if (a.d_weights && lane < n) {
+            id = a.ids[t0 * topk + lane];
+            dw = a.d_weights[t0 * topk + lane];
+        }
+        if (first && a.d_losses) {
+            const int tokens = a.counts[experts];
+            const float inv = tokens > 0 ? 1.0f / (float)tokens : 0.0f;
+            const float c = a.d_losses[0] * ((float)experts / (float)topk) * inv * inv;
+            zc = 2.0f * a.d_losses[1] * inv;
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+                load[i] = pos * V + i < experts ? c * (float)a.counts[pos * V + i] : 0.0f;
+        }
+        first = false;
         const bool live = lse != -__builtin_inff();
         float x[V];
-        if (live)
-            ld_logits<DT, V>(static_cast<const char*>(a.logits) + t * a.ld * Elem<DT>::kBytes, pos, experts, x);
+        logits_of<DT, V>(raw, pos, experts, x);
         if (a.d_weights) {
+            wave_sync();
 #pragma unroll
             for (int i = 0; i < V; ++i)
                 grad[(sub * G + pos) * V + i] = kNone;
             wave_sync();
-            const size_t left = a.tokens - t0;
-            const int n = (left < (size_t)TW ? (int)left : TW) * topk;
             for (int i = lane; i < n; i += kWave) {
-                const int id = a.ids[t0 * topk + i];
+                if (i >= kWave) {
+                    id = a.ids[t0 * topk + i];
+                    dw = a.d_weights[t0 * topk + i];
+                }
                 if (id >= 0 && id < experts)
-                    grad[i / topk * (G * V) + id] = __builtin_bit_cast(uint32_t, a.d_weights[t0 * topk + i]);
+                    grad[i / topk * (G * V) + id] = __builtin_bit_cast(uint32_t, dw);
             }
             wave_sync();
         }
@@ -324,7 +449,7 @@ __global__ __launch_bounds__(kRouteWaves * kWave) void k_route_backward(RouteBwd
         bool chosen[V];
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            p[i] = live && pos * V + i < experts ? expf(x[i] - lse) : 0.0f;
+            p[i] = expf(live && pos * V + i < experts ? x[i] - lse : -__builtin_inff());
             const uint32_t g = a.d_weights ? grad[(sub * G + pos) * V + i] : kNone;
             chosen[i] = g != kNone;
             const float w = chosen[i] ? bits_f32(g) : 0.0f;
@@ -369,12 +494,24 @@ int lanes_for(int experts)
     return g;
 }
 
-// Workgroups of a call: every wave its tokens once, up to four workgroups a CU.
-uint32_t route_grid(size_t tokens, int experts)
+// Waves and workgroups of a call. With sums a workgroup a CU, so that there are
+// few parts to add, and one for up to 16 waves of tokens, which then needs no
+// second launch; without, four waves a workgroup.
+struct Spread {
+    unsigned threads;
+    uint32_t grid;
+};
+Spread spread(size_t tokens, int experts, bool sums)
 {
-    const size_t per = (size_t)kRouteWaves * (kWave / lanes_for(experts));
-    const size_t want = (tokens + per - 1) / per, most = 4 * (size_t)device_cu_count();
-    return (uint32_t)(want < 1 ? 1 : want < most ? want : most);
+    const size_t most = !sums ? 4 : experts > 512 ? 8 : 16, all = (size_t)device_cu_count(), cus = !sums ? 8 * all : all < 1024 ? all : 1024;
+    const size_t per = (size_t)(kWave / lanes_for(experts)), units = tokens ? (tokens + per - 1) / per : 1;
+    size_t w = units < most ? units : most;
+    if (sums && units > most) {   // every CU before a second wave on one
+        w = (units + cus - 1) / cus;
+        w = w < 4 ? 4 : w < most ? w : most;
+    }
+    const size_t want = (units + w - 1) / w;
+    return {(unsigned)(w * kWave), (uint32_t)(want < cus ? want : cus)};
 }
 
 template <int DT, bool SUMS>
@@ -413,21 +550,22 @@ const void* route_backward_fn(int experts)
 
 size_t route_workspace_words(size_t tokens, int experts)
 {
-    return 1 + (size_t)route_grid(tokens, experts) * (2 * (size_t)experts + 2);
+    return 1 + spread(tokens, experts, true).grid * (part_words(experts) + 2) + (size_t)(experts + kSumExperts - 1) / kSumExperts;
 }
 
 hipError_t launch_route(const RouteArgs& in, int dtype, hipStream_t s)
 {
     RouteArgs a = in;
     void* params[] = {&a};
-    a.parts = route_grid(a.tokens, a.experts);
+    const Spread sp = spread(a.tokens, a.experts, a.counts);
+    a.parts = sp.grid;
     const void* fn = a.counts ? dtype ? route_fn<1, true>(a.experts) : route_fn<0, true>(a.experts)
                      : dtype  ? route_fn<1, false>(a.experts)
                               : route_fn<0, false>(a.experts);
-    const hipError_t e = launch_logged("k_route", fn, dim3(a.parts), dim3(kRouteWaves * kWave), params, s);
-    if (e != hipSuccess || !a.counts)
+    const hipError_t e = launch_logged("k_route", fn, dim3(sp.grid), dim3(sp.threads), params, s);
+    if (e != hipSuccess || !a.counts || sp.grid == 1)
         return e;
-    return launch_logged("k_route_sums", (const void*)k_route_sums, dim3(1), dim3(1024), params, s);
+    return launch_logged("k_route_sums", (const void*)k_route_sums, dim3((unsigned)(a.experts + kSumExperts - 1) / kSumExperts), dim3(1024), params, s);
 }
 
 hipError_t launch_route_backward(const RouteBwdArgs& in, int dtype, hipStream_t s)
@@ -435,7 +573,7 @@ hipError_t launch_route_backward(const RouteBwdArgs& in, int dtype, hipStream_t 
     RouteBwdArgs a = in;
     void* params[] = {&a};
     const void* fn = dtype ? route_backward_fn<1>(a.experts) : route_backward_fn<0>(a.experts);
-    return launch_logged("k_route_backward", fn, dim3(route_grid(a.tokens, a.experts)), dim3(kRouteWaves * kWave), params, s);
+    return launch_logged("k_route_backward", fn, dim3(spread(a.tokens, a.experts, false).grid), dim3(256), params, s);
 }
 
 }  // namespace rx

@@ -74,6 +74,18 @@ __device__ __forceinline__ float value_of(uint32_t key)
     return bits_f32(DT == 0 ? u : u & 0xFFFF0000u);
 }
 
+// exp of d <= 0 in six instructions: 2^y with y the rounded d log2 e, and what the
+// rounding left as a factor of 1 + r ln 2. v_exp_f32 is within a unit, the factor
+// within half of one; values below 2^-126 become 0, and a NaN too.
+__device__ __forceinline__ float exp_of(float d)
+{
+    d = fmaxf(d, -150.0f);
+    const float y = d * 1.44269502f;
+    const float r = __builtin_fmaf(d, 1.92596299e-8f, __builtin_fmaf(d, 1.44269502f, -y));
+    const float e = __builtin_amdgcn_exp2f(y);
+    return __builtin_fmaf(e, r * 0.693147182f, e);
+}
+
 // The workspace: a counter; for each workgroup a part (experts counts, experts
 // sums of P), then for each its tokens and the sum of their lse^2; and a sum for
 // each workgroup of the second launch.
@@ -169,7 +181,7 @@ __global__ __launch_bounds__(kRouteWaves<V> * kWave) void k_route(RouteArgs a)
         float sum = 0.0f, e[V];
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            e[i] = expf(key[i] ? x[i] - high : -__builtin_inff());   // 0 for an empty token
+            e[i] = exp_of(key[i] ? x[i] - high : -__builtin_inff());   // 0 for an empty token
             sum += e[i];
         }
         sum = group_sum<G>(sum);
@@ -396,7 +408,7 @@ __global__ __launch_bounds__(256) void k_route_backward(RouteBwdArgs a)
 {
     constexpr int TW = kWave / G, VE = Elem<DT>::kVE, kWaves = 4;
     constexpr uint32_t kNone = 0x7FFFDEADu;   // no choice: a NaN that no gradient has
-    __shared__ uint32_t grads[kWaves][TW * G * V];
+    __shared__ __align__(16) uint32_t grads[kWaves][TW * G * V];
     const int lane = lane_id(), wave = threadIdx.x / kWave, pos = lane % G, sub = lane / G;
     const int experts = a.experts, topk = a.topk;
     float load[V] = {}, zc = 0.0f;
@@ -407,23 +419,28 @@ __global__ __launch_bounds__(256) void k_route_backward(RouteBwdArgs a)
         // all loads before anything waits
         const size_t t = t0 + sub, row = t < a.tokens ? t : a.tokens - 1;
         const RawLogits<DT, V> raw = ld_logits<DT, V>(static_cast<const char*>(a.logits) + row * a.ld * Elem<DT>::kBytes, pos, experts);
-        const float lse = t < a.tokens ? a.lse[row] : -__builtin_inff();
+        const float stored = a.lse[row], lse = t < a.tokens ? stored : -__builtin_inff();
         const size_t left = a.tokens - t0;
         const int n = (left < (size_t)TW ? (int)left : TW) * topk;
         int id = -1;
         float dw = 0.0f;
-        if (a.d_weights && lane < n) {
-            id = a.ids[t0 * topk + lane];
-            dw = a.d_weights[t0 * topk + lane];
+        if (a.d_weights) {
+            const size_t at = t0 * topk + (lane < n ? lane : 0);
+            id = a.ids[at];
+            dw = a.d_weights[at];
         }
         if (first && a.d_losses) {
-            const int tokens = a.counts[experts];
-            const float inv = tokens > 0 ? 1.0f / (float)tokens : 0.0f;
-            const float c = a.d_losses[0] * ((float)experts / (float)topk) * inv * inv;
-            zc = 2.0f * a.d_losses[1] * inv;
+            u32x4 c[V / 4];
 #pragma unroll
-            for (int i = 0; i < V; ++i)
-                load[i] = pos * V + i < experts ? c * (float)a.counts[pos * V + i] : 0.0f;
+            for (int i = 0; i < V / 4; ++i)
+                c[i] = ld_raw<0, true>(a.counts, pos * (V / 4) + i, experts);
+            const int tokens = a.counts[experts];
+            const float d0 = a.d_losses[0], d1 = a.d_losses[1], inv = tokens > 0 ? 1.0f / (float)tokens : 0.0f;
+            const float by = d0 * ((float)experts / (float)topk) * inv * inv;
+            zc = 2.0f * d1 * inv;
+#pragma unroll
+            for (int i = 0; i < V; ++i)   // 0 past the experts
+                load[i] = by * (float)(int)fixed<0, true>(c[i / 4], pos * (V / 4) + i / 4, experts)[i % 4];
         }
         first = false;
         const bool live = lse != -__builtin_inff();
@@ -440,26 +457,30 @@ __global__ __launch_bounds__(256) void k_route_backward(RouteBwdArgs a)
                     id = a.ids[t0 * topk + i];
                     dw = a.d_weights[t0 * topk + i];
                 }
-                if (id >= 0 && id < experts)
+                if (i < n && id >= 0 && id < experts)
                     grad[i / topk * (G * V) + id] = __builtin_bit_cast(uint32_t, dw);
             }
             wave_sync();
         }
+        u32x4 got[V / 4];
+#pragma unroll
+        for (int i = 0; i < V / 4; ++i)
+            got[i] = u32x4{kNone, kNone, kNone, kNone};
+        if (a.d_weights)
+#pragma unroll
+            for (int i = 0; i < V / 4; ++i)
+                got[i] = *reinterpret_cast<const u32x4*>(&grad[(sub * G + pos) * V + 4 * i]);
         float p[V], d[V], dot = 0.0f, share = 0.0f, mean = 0.0f;
         bool chosen[V];
 #pragma unroll
         for (int i = 0; i < V; ++i) {
             p[i] = expf(live && pos * V + i < experts ? x[i] - lse : -__builtin_inff());
-            const uint32_t g = a.d_weights ? grad[(sub * G + pos) * V + i] : kNone;
+            const uint32_t g = got[i / 4][i % 4];
             chosen[i] = g != kNone;
             const float w = chosen[i] ? bits_f32(g) : 0.0f;
-            d[i] = load[i];
-            if (a.renormalize) {
-                share += chosen[i] ? p[i] : 0.0f;
-                mean += p[i] * w;
-            } else {
-                d[i] += w;
-            }
+            share += chosen[i] ? p[i] : 0.0f;
+            mean += p[i] * w;
+            d[i] = load[i] + (a.renormalize ? 0.0f : w);
             dot += p[i] * d[i];
             x[i] = w;
         }
@@ -485,49 +506,64 @@ __global__ __launch_bounds__(256) void k_route_backward(RouteBwdArgs a)
     }
 }
 
-// Lanes a token: eight logits each, sixteen beyond 512 experts.
-int lanes_for(int experts)
+// Lanes a token with v logits each.
+int lanes_for(int experts, int v)
 {
     int g = 1;
-    while (g < kWave && g * 8 < experts)
+    while (g < kWave && g * v < experts)
         g *= 2;
     return g;
 }
 
-// Waves and workgroups of a call. With sums a workgroup a CU, so that there are
-// few parts to add, and one for up to 16 waves of tokens, which then needs no
-// second launch; without, four waves a workgroup.
+// Waves and workgroups of a call, and the logits of a lane. Sixteen logits a lane
+// cost a token less (a round of choices 46 instructions for twice the tokens
+// instead of 38), eight have more waves and a shorter way: sixteen beyond 512
+// experts, and where eight would take over twelve waves a CU (16384 x
+// 128 BF16 with sums: 10.3 against 11.2 us).
+// With sums a workgroup a CU, so that there are few parts to add, and one for up
+// to 16 waves of tokens, which then needs no second launch; without, four waves a
+// workgroup.
 struct Spread {
+    int v;
     unsigned threads;
     uint32_t grid;
 };
 Spread spread(size_t tokens, int experts, bool sums)
 {
-    const size_t most = !sums ? 4 : experts > 512 ? 8 : 16, all = (size_t)device_cu_count(), cus = !sums ? 8 * all : all < 1024 ? all : 1024;
-    const size_t per = (size_t)(kWave / lanes_for(experts)), units = tokens ? (tokens + per - 1) / per : 1;
+    const size_t all = (size_t)device_cu_count(), cus = !sums ? 8 * all : all < 1024 ? all : 1024;
+    auto units_of = [&](int v) {
+        const size_t per = (size_t)(kWave / lanes_for(experts, v));
+        return tokens ? (tokens + per - 1) / per : 1;
+    };
+    const int v = experts > 512 || units_of(8) > 12 * all ? 16 : 8;
+    const size_t units = units_of(v), most = !sums ? 4 : v == 16 ? 8 : 16;
     size_t w = units < most ? units : most;
     if (sums && units > most) {   // every CU before a second wave on one
         w = (units + cus - 1) / cus;
         w = w < 4 ? 4 : w < most ? w : most;
     }
     const size_t want = (units + w - 1) / w;
-    return {(unsigned)(w * kWave), (uint32_t)(want < cus ? want : cus)};
+    return {v, (unsigned)(w * kWave), (uint32_t)(want < cus ? want : cus)};
 }
 
-template <int DT, bool SUMS>
+template <int DT, bool SUMS, int V>
 const void* route_fn(int experts)
 {
-    if (experts > 512)
-        return (const void*)k_route<DT, 64, 16, SUMS>;
-    switch (lanes_for(experts)) {
-    case 1: return (const void*)k_route<DT, 1, 8, SUMS>;
-    case 2: return (const void*)k_route<DT, 2, 8, SUMS>;
-    case 4: return (const void*)k_route<DT, 4, 8, SUMS>;
-    case 8: return (const void*)k_route<DT, 8, 8, SUMS>;
-    case 16: return (const void*)k_route<DT, 16, 8, SUMS>;
-    case 32: return (const void*)k_route<DT, 32, 8, SUMS>;
-    default: return (const void*)k_route<DT, 64, 8, SUMS>;
+    switch (lanes_for(experts, V)) {
+    case 1: return (const void*)k_route<DT, 1, V, SUMS>;
+    case 2: return (const void*)k_route<DT, 2, V, SUMS>;
+    case 4: return (const void*)k_route<DT, 4, V, SUMS>;
+    case 8: return (const void*)k_route<DT, 8, V, SUMS>;
+    case 16: return (const void*)k_route<DT, 16, V, SUMS>;
+    case 32: return (const void*)k_route<DT, 32, V, SUMS>;
+    default: return (const void*)k_route<DT, 64, V, SUMS>;
     }
+}
+template <int DT>
+const void* route_fn(int experts, int v, bool sums)
+{
+    return v == 16 ? sums ? route_fn<DT, true, 16>(experts) : route_fn<DT, false, 16>(experts)
+                   : sums ? route_fn<DT, true, 8>(experts) : route_fn<DT, false, 8>(experts);
 }
 
 template <int DT>
@@ -535,7 +571,7 @@ const void* route_backward_fn(int experts)
 {
     if (experts > 512)
         return (const void*)k_route_backward<DT, 64, 16>;
-    switch (lanes_for(experts)) {
+    switch (lanes_for(experts, 8)) {
     case 1: return (const void*)k_route_backward<DT, 1, 8>;
     case 2: return (const void*)k_route_backward<DT, 2, 8>;
     case 4: return (const void*)k_route_backward<DT, 4, 8>;
@@ -559,9 +595,7 @@ hipError_t launch_route(const RouteArgs& in, int dtype, hipStream_t s)
     void* params[] = {&a};
     const Spread sp = spread(a.tokens, a.experts, a.counts);
     a.parts = sp.grid;
-    const void* fn = a.counts ? dtype ? route_fn<1, true>(a.experts) : route_fn<0, true>(a.experts)
-                     : dtype  ? route_fn<1, false>(a.experts)
-                              : route_fn<0, false>(a.experts);
+    const void* fn = dtype ? route_fn<1>(a.experts, sp.v, a.counts) : route_fn<0>(a.experts, sp.v, a.counts);
     const hipError_t e = launch_logged("k_route", fn, dim3(sp.grid), dim3(sp.threads), params, s);
     if (e != hipSuccess || !a.counts || sp.grid == 1)
         return e;
@@ -573,7 +607,9 @@ hipError_t launch_route_backward(const RouteBwdArgs& in, int dtype, hipStream_t 
     RouteBwdArgs a = in;
     void* params[] = {&a};
     const void* fn = dtype ? route_backward_fn<1>(a.experts) : route_backward_fn<0>(a.experts);
-    return launch_logged("k_route_backward", fn, dim3(spread(a.tokens, a.experts, false).grid), dim3(256), params, s);
+    const size_t per = 4 * (size_t)(kWave / lanes_for(a.experts, a.experts > 512 ? 16 : 8));   // tokens of a workgroup
+    const size_t want = (a.tokens + per - 1) / per, most = 8 * (size_t)device_cu_count();
+    return launch_logged("k_route_backward", fn, dim3((unsigned)(want < most ? want : most)), dim3(256), params, s);
 }
 
 }  // namespace rx

@@ -179,6 +179,101 @@ __device__ __forceinline__ uint32_t wave_sum_u(uint32_t v)
     return q[0] + q[1];
 }
 
+// Sum over aligned groups of G lanes, the same in each of them.
+template <int G>
+__device__ __forceinline__ float group_sum(float v)
+{
+    auto u = [](float x) { return __builtin_bit_cast(uint32_t, x); };
+    if constexpr (G >= 2) v += bits_f32(dpp<0xB1>(u(v)));
+    if constexpr (G >= 4) v += bits_f32(dpp<0x4E>(u(v)));
+    if constexpr (G >= 8) v += bits_f32(dpp<0x141>(u(v)));
+    if constexpr (G >= 16) v += bits_f32(dpp<0x140>(u(v)));
+    if constexpr (G >= 32) {
+        auto p = __builtin_amdgcn_permlane16_swap(u(v), u(v), false, false);
+        v = bits_f32(p[0]) + bits_f32(p[1]);
+    }
+    if constexpr (G >= 64) {
+        auto p = __builtin_amdgcn_permlane32_swap(u(v), u(v), false, false);
+        v = bits_f32(p[0]) + bits_f32(p[1]);
+    }
+    return v;
+}
+
+// ... of a number of lanes that is the same for the wave.
+__device__ __forceinline__ float group_sum_rt(float v, int g)
+{
+    auto u = [](float x) { return __builtin_bit_cast(uint32_t, x); };
+    if (g >= 2) v += bits_f32(dpp<0xB1>(u(v)));
+    if (g >= 4) v += bits_f32(dpp<0x4E>(u(v)));
+    if (g >= 8) v += bits_f32(dpp<0x141>(u(v)));
+    if (g >= 16) v += bits_f32(dpp<0x140>(u(v)));
+    if (g >= 32) {
+        auto p = __builtin_amdgcn_permlane16_swap(u(v), u(v), false, false);
+        v = bits_f32(p[0]) + bits_f32(p[1]);
+    }
+    if (g >= 64) {
+        auto p = __builtin_amdgcn_permlane32_swap(u(v), u(v), false, false);
+        v = bits_f32(p[0]) + bits_f32(p[1]);
+    }
+    return v;
+}
+
+// Sum over the lanes at this one's place in each group of G, the same in all.
+template <int G>
+__device__ __forceinline__ float across(float v)
+{
+    auto u = [](float x) { return __builtin_bit_cast(uint32_t, x); };
+    if constexpr (G <= 1) v += bits_f32(dpp<0x121>(u(v)));   // row_ror 1, 2, 4, 8
+    if constexpr (G <= 2) v += bits_f32(dpp<0x122>(u(v)));
+    if constexpr (G <= 4) v += bits_f32(dpp<0x124>(u(v)));
+    if constexpr (G <= 8) v += bits_f32(dpp<0x128>(u(v)));
+    if constexpr (G <= 16) {
+        auto p = __builtin_amdgcn_permlane16_swap(u(v), u(v), false, false);
+        v = bits_f32(p[0]) + bits_f32(p[1]);
+    }
+    if constexpr (G <= 32) {
+        auto p = __builtin_amdgcn_permlane32_swap(u(v), u(v), false, false);
+        v = bits_f32(p[0]) + bits_f32(p[1]);
+    }
+    return v;
+}
+template <int G>
+__device__ __forceinline__ uint32_t across(uint32_t v)
+{
+    if constexpr (G <= 1) v += dpp<0x121>(v);
+    if constexpr (G <= 2) v += dpp<0x122>(v);
+    if constexpr (G <= 4) v += dpp<0x124>(v);
+    if constexpr (G <= 8) v += dpp<0x128>(v);
+    if constexpr (G <= 16) {
+        auto p = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+        v = p[0] + p[1];
+    }
+    if constexpr (G <= 32) {
+        auto p = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+        v = p[0] + p[1];
+    }
+    return v;
+}
+
+// ... of a number of lanes that is the same for the wave.
+__device__ __forceinline__ float across_rt(float v, int g)
+{
+    auto u = [](float x) { return __builtin_bit_cast(uint32_t, x); };
+    if (g <= 1) v += bits_f32(dpp<0x121>(u(v)));
+    if (g <= 2) v += bits_f32(dpp<0x122>(u(v)));
+    if (g <= 4) v += bits_f32(dpp<0x124>(u(v)));
+    if (g <= 8) v += bits_f32(dpp<0x128>(u(v)));
+    if (g <= 16) {
+        auto p = __builtin_amdgcn_permlane16_swap(u(v), u(v), false, false);
+        v = bits_f32(p[0]) + bits_f32(p[1]);
+    }
+    if (g <= 32) {
+        auto p = __builtin_amdgcn_permlane32_swap(u(v), u(v), false, false);
+        v = bits_f32(p[0]) + bits_f32(p[1]);
+    }
+    return v;
+}
+
 // What the wave's lanes wrote to LDS is there for all of them: its LDS
 // instructions run in order, so only the compiler has to keep theirs.
 __device__ __forceinline__ void wave_sync()

@@ -22,30 +22,46 @@ __device__ __forceinline__ int inside(int v, int hidden)
     return TAIL ? left : left > 0 ? VE : 0;
 }
 
+// The call's dropper: asked for at a kernel's start, long before it is used.
 template <class A>
-__device__ __forceinline__ Dropper dropper(const A& a, size_t row)
+__device__ __forceinline__ Dropper dropper(const A& a)
 {
     Dropper d = {};
     if (a.threshold) {
         d.seed = a.rng[0];
         d.offset = a.rng[1];
-        d.first = row * ((a.hidden + 7) / 8);
         d.threshold = a.threshold;
     }
     return d;
 }
+__device__ __forceinline__ void at_row(Dropper& d, size_t row, size_t hidden) { d.first = row * ((hidden + 7) / 8); }
 
 // Loads ahead as in k_norm: with one vector a thread, everything before the
-// sources.
-template <int DT, bool TAIL, int NV, int WG>
+// sources. NARROW: a row has a.lanes of a wave's lanes, a power of two, and a wave
+// 64 / a.lanes rows (16000 x 64 BF16 with residual, bias and dropout: 5.3 us, 11.9 with a
+// workgroup a row).
+template <int DT, bool TAIL, int NV, int WG, bool NARROW>
 __global__ __launch_bounds__(WG) void k_layer_norm(LayerNormArgs a)
 {
     constexpr int VE = Elem<DT>::kVE, EB = Elem<DT>::kBytes;
     constexpr bool kAhead = NV == 1;
     __shared__ float lds[2 * 16];
     int turn = 0;
-    const size_t t = blockIdx.x;
-    const int hidden = (int)a.hidden, tid = (int)threadIdx.x, bd = (int)blockDim.x;
+    const int hidden = (int)a.hidden, bd = NARROW ? a.lanes : (int)blockDim.x;
+    const int tid = NARROW ? (int)threadIdx.x & (bd - 1) : (int)threadIdx.x;
+    size_t t = blockIdx.x;
+    if (NARROW) {
+        t = t * (WG / bd) + threadIdx.x / bd;
+        if (t >= a.rows)   // whole groups of lanes, which share nothing with the others
+            return;
+    }
+    auto row_sum = [&](float& v) {
+        if (NARROW)
+            v = group_sum_rt(v, bd);
+        else
+            block_sums<1>(&v, lds, turn);
+    };
+    Dropper d = dropper(a);
     u32x4 res[NV], wv[NV], bv[NV], biasv[NV];
     auto load = [&](u32x4* to, const void* row) {
 #pragma unroll
@@ -63,7 +79,7 @@ __global__ __launch_bounds__(WG) void k_layer_norm(LayerNormArgs a)
         if (a.b) load(bv, a.b);
     }
     float y[NV][VE];
-    fold_row<DT, TAIL, NV>(a.src, a.nsrc, t * a.ld_src * EB, hidden, y);
+    fold_row<DT, TAIL, NV>(a.src, a.nsrc, t * a.ld_src * EB, hidden, tid, bd, y);
     if (a.bias) {
         if (!kAhead) load(biasv, a.bias);
 #pragma unroll
@@ -76,7 +92,7 @@ __global__ __launch_bounds__(WG) void k_layer_norm(LayerNormArgs a)
         }
     }
     if (a.threshold) {
-        const Dropper d = dropper(a, t);
+        at_row(d, t, a.hidden);
 #pragma unroll
         for (int u = 0; u < NV; ++u)
             drop_vector<DT>(d, tid + u * bd, a.gain, y[u]);
@@ -109,7 +125,7 @@ __global__ __launch_bounds__(WG) void k_layer_norm(LayerNormArgs a)
         for (int k = 0; k < VE; ++k)
             s += k < n ? y[u][k] : 0.0f;
     }
-    block_sums<1>(&s, lds, turn);
+    row_sum(s);
     const float mean = s * a.inv_hidden;
     float q = 0.0f;
 #pragma unroll
@@ -121,7 +137,7 @@ __global__ __launch_bounds__(WG) void k_layer_norm(LayerNormArgs a)
             q += k < n ? y[u][k] * y[u][k] : 0.0f;
         }
     }
-    block_sums<1>(&q, lds, turn);
+    row_sum(q);
     const float rstd = 1.0f / __builtin_sqrtf(q * a.inv_hidden + a.eps);
     if (tid == 0) {
         if (a.mean)
@@ -204,6 +220,7 @@ __global__ __launch_bounds__(256) void k_layer_norm_columns(LayerNormBwdArgs a)
     const int hidden = (int)a.hidden, lane = lane_id(), wave = threadIdx.x / kWave;
     const int v = (int)blockIdx.x * kWave + lane;
     const size_t r0 = blockIdx.y * a.part_rows, r1 = r0 + a.part_rows < a.rows ? r0 + a.part_rows : a.rows;
+    Dropper d = dropper(a);
     float w[VE], acc[3][VE] = {};
 #pragma unroll
     for (int k = 0; k < VE; ++k)
@@ -231,8 +248,10 @@ __global__ __launch_bounds__(256) void k_layer_norm_columns(LayerNormBwdArgs a)
         }
         if (a.d_residual)
             st_row<DT, TAIL, true>(static_cast<char*>(a.d_residual) + t * a.ld_d_residual * EB, v, hidden, pack<DT>(o));
-        if (a.threshold)
-            drop_vector<DT>(dropper(a, t), v, a.gain, o);
+        if (a.threshold) {
+            at_row(d, t, a.hidden);
+            drop_vector<DT>(d, v, a.gain, o);
+        }
 #pragma unroll
         for (int k = 0; k < VE; ++k)
             acc[2][k] += o[k];
@@ -260,24 +279,27 @@ __global__ __launch_bounds__(256) void k_layer_norm_columns(LayerNormBwdArgs a)
 
 // A row's vectors in registers, its two sums across the threads that hold it, and
 // the parameters' sums of a range of rows (a part) in registers too: every input is
-// read once. R teams of WG / R threads have a row each. The next row's loads go out
+// read once. Several teams of a.lanes lanes (a power of two up to a wave) have a row
+// each where TEAMS; the next row's loads go out
 // as soon as this row's are unpacked, before its sums and stores. 16384 x 8192 BF16
 // with dropout and all outputs: 250 us for 1.34 GB (5.4 TB/s), 340 by k_layer_norm_means and
 // k_layer_norm_columns, which read h and d_z twice.
-template <int DT, bool TAIL, int NV, int WG, int R, bool DROP>
+template <int DT, bool TAIL, int NV, int WG, bool TEAMS, bool DROP>
 __global__ __launch_bounds__(WG, WG > 512 ? 4 : 2) void k_layer_norm_backward(LayerNormBwdArgs a)
 {
-    constexpr int VE = Elem<DT>::kVE, EB = Elem<DT>::kBytes, W = WG / R, E = NV * VE;
-    static_assert(R == 1 || W == kWave, "teams of several waves share no barriers");
+    constexpr int VE = Elem<DT>::kVE, EB = Elem<DT>::kBytes, E = NV * VE;
     __shared__ float sums[2 * 16 * 2];
-    __shared__ float join[R > 1 ? R * W * VE : 1];
+    __shared__ float join[TEAMS ? WG * VE : 1];
     int turn = 0;
     const int hidden = (int)a.hidden;
-    const int team = R == 1 ? 0 : (int)__builtin_amdgcn_readfirstlane(threadIdx.x / W);
-    const int tid = (int)threadIdx.x - team * W;
+    const int W = TEAMS ? a.lanes : WG, R = WG / W, tid = TEAMS ? (int)threadIdx.x & (W - 1) : (int)threadIdx.x;
+    const int team = TEAMS ? W == kWave ? (int)__builtin_amdgcn_readfirstlane(threadIdx.x / kWave) : (int)threadIdx.x / W : 0;
     const size_t r0 = blockIdx.x * a.part_rows, r1 = r0 + a.part_rows < a.rows ? r0 + a.part_rows : a.rows;
     const u32x4 zero = {0, 0, 0, 0};
     const uint32_t one = DT ? 0x3F803F80u : 0x3F800000u;
+    Dropper d = {};
+    if (DROP)
+        d = dropper(a);
     u32x4 w[NV], hv[NV], dhv[NV], dzv[NV];
     float acc_w[E] = {}, acc_b[E] = {}, acc_bias[E] = {};
 #pragma unroll
@@ -323,11 +345,15 @@ __global__ __launch_bounds__(WG, WG > 512 ? 4 : 2) void k_layer_norm_backward(La
         }
         if (t + R < r1)
             load(t + R);
-        block_sums<2, W / kWave>(s, sums, turn);
+        if constexpr (TEAMS) {
+            s[0] = group_sum_rt(s[0], W);
+            s[1] = group_sum_rt(s[1], W);
+        } else {
+            block_sums<2, WG / kWave>(s, sums, turn);
+        }
         const float m1 = s[0] * a.inv_hidden, m2 = s[1] * a.inv_hidden;
-        Dropper d;
         if (DROP)
-            d = dropper(a, t);
+            at_row(d, t, a.hidden);
 #pragma unroll
         for (int u = 0; u < NV; ++u) {
             const int v = tid + u * W;
@@ -350,22 +376,29 @@ __global__ __launch_bounds__(WG, WG > 512 ? 4 : 2) void k_layer_norm_backward(La
 #pragma unroll
     for (int p = 0; p < 3; ++p) {
         float* acc = p == 0 ? acc_w : p == 1 ? acc_b : acc_bias;
-        float* to = a.parts + (blockIdx.x * 3 + p) * a.hidden;
-        if ((p == 0 && !a.d_w) || (p == 1 && !a.d_b) || (p == 2 && !a.d_bias))
+        float* to = p == 0 ? a.d_w : p == 1 ? a.d_b : a.d_bias;
+        if (!to)
             continue;
+        if (a.nparts > 1)
+            to = a.parts + (blockIdx.x * 3 + p) * a.hidden;
 #pragma unroll
         for (int u = 0; u < NV; ++u) {
-            if constexpr (R > 1) {   // the teams in their order
+            if constexpr (TEAMS) {   // a wave's teams, then the waves in their order
+                const int wave = threadIdx.x / kWave, lane = lane_id();
                 __syncthreads();
 #pragma unroll
                 for (int k = 0; k < VE; ++k)
-                    join[(team * VE + k) * W + tid] = acc[u * VE + k];
+                    join[(wave * VE + k) * kWave + lane] = across_rt(acc[u * VE + k], W);
                 __syncthreads();
                 if (team == 0)
 #pragma unroll
-                    for (int k = 0; k < VE; ++k)
-                        for (int r = 1; r < R; ++r)
-                            acc[u * VE + k] += join[(r * VE + k) * W + tid];
+                    for (int k = 0; k < VE; ++k) {
+                        float v = join[k * kWave + lane];
+#pragma unroll
+                        for (int r = 1; r < WG / kWave; ++r)
+                            v += join[(r * VE + k) * kWave + lane];
+                        acc[u * VE + k] = v;
+                    }
             }
             const int c = (tid + u * W) * VE;
             if (team == 0) {
@@ -416,12 +449,15 @@ __global__ __launch_bounds__(1024) void k_layer_norm_params(LayerNormBwdArgs a)
     to[c] = s;
 }
 
-template <int NV, int WG>
+template <int NV, int WG, bool NARROW = false>
 const void* forward_of(int dtype, bool tail)
 {
     if (dtype == 0)
-        return tail ? (const void*)k_layer_norm<0, true, NV, WG> : (const void*)k_layer_norm<0, false, NV, WG>;
-    return tail ? (const void*)k_layer_norm<1, true, NV, WG> : (const void*)k_layer_norm<1, false, NV, WG>;
+        return tail ? (const void*)k_layer_norm<0, true, NV, WG, NARROW> : (const void*)k_layer_norm<0, false, NV, WG, NARROW>;
+    if constexpr (NV > 4)
+        return nullptr;   // 32768 elements are four vectors a thread
+    else
+        return tail ? (const void*)k_layer_norm<1, true, NV, WG, NARROW> : (const void*)k_layer_norm<1, false, NV, WG, NARROW>;
 }
 const void* forward_fn(int dtype, bool tail, unsigned wg, size_t nvec)
 {
@@ -442,13 +478,22 @@ unsigned forward_threads(size_t nvec, size_t rows)
     return t >= 1024 ? 1024u : t < kWave ? (unsigned)kWave : (unsigned)((t + kWave - 1) / kWave * kWave);
 }
 
-// How a gradient's rows are spread. Rows of up to 128 vectors take a wave each, eight
-// to a workgroup; longer ones two vectors a thread, and workgroups of 512 threads a
+// Lanes of a row of up to a wave's vectors: the next power of two.
+int narrow_lanes(size_t nvec)
+{
+    int g = 1;
+    while (g < kWave && (size_t)g < nvec)
+        g *= 2;
+    return g;
+}
+
+// How a gradient's rows are spread. Rows of up to 128 vectors take a wave's lanes or
+// fewer, in workgroups of 512 threads; longer ones two vectors a thread, and workgroups of 512 threads a
 // CU or one larger one: every part costs its sums' write and read. Rows beyond
 // what the registers hold (1024 vectors BF16, FP32 2048) go by columns in parts.
 struct Spread {
     bool whole;                // k_layer_norm_backward
-    unsigned threads, teams;   // of a row, rows of a workgroup
+    unsigned threads, lanes;   // of a workgroup; of a row where it has several, else 0
     int nv;                    // vectors a thread
     size_t part_rows, parts;
 };
@@ -461,9 +506,18 @@ Spread spread(size_t rows, size_t hidden, int dtype)
     if (s.whole) {
         s.threads = threads_for((nvec + 1) / 2, 512);
         s.nv = (int)((nvec + s.threads - 1) / s.threads);
-        s.teams = s.threads == kWave ? 8 : 1;
-        const size_t wg = s.threads * s.teams;
-        want = cus * (wg < 512 ? 512 / wg : 1);
+        size_t teams = 1;
+        if (s.threads == kWave) {
+            s.threads = 512;
+            s.lanes = (unsigned)narrow_lanes(nvec);
+            teams = 512 / s.lanes;
+        }
+        want = cus * ((s.lanes && s.nv == 1 ? 1024 : 512) / s.threads);   // what the registers leave room for
+        // every team a row, and up to two rows each one part, whose sums need no second launch
+        if (want > (rows + teams - 1) / teams)
+            want = (rows + teams - 1) / teams;
+        if (rows <= 2 * teams)
+            want = 1;
     } else {
         const size_t blocks = (nvec + kWave - 1) / kWave;   // about four workgroups a CU over all columns
         want = (4 * cus + blocks - 1) / blocks;
@@ -482,16 +536,16 @@ Spread spread(size_t rows, size_t hidden, int dtype)
 template <int DT, bool TAIL, bool DROP>
 const void* backward_fn(const Spread& s)
 {
-    if (s.threads == 64)
-        return s.nv == 1 ? (const void*)k_layer_norm_backward<DT, TAIL, 1, 512, 8, DROP> : (const void*)k_layer_norm_backward<DT, TAIL, 2, 512, 8, DROP>;
+    if (s.lanes)
+        return s.nv == 1 ? (const void*)k_layer_norm_backward<DT, TAIL, 1, 512, true, DROP> : (const void*)k_layer_norm_backward<DT, TAIL, 2, 512, true, DROP>;
     if (s.threads == 128)
-        return (const void*)k_layer_norm_backward<DT, TAIL, 2, 128, 1, DROP>;
+        return (const void*)k_layer_norm_backward<DT, TAIL, 2, 128, false, DROP>;
     if (s.threads == 256)
-        return (const void*)k_layer_norm_backward<DT, TAIL, 2, 256, 1, DROP>;
+        return (const void*)k_layer_norm_backward<DT, TAIL, 2, 256, false, DROP>;
     if constexpr (DT == 0)
         if (s.nv > 2)
-            return (const void*)k_layer_norm_backward<DT, TAIL, 4, 512, 1, DROP>;
-    return (const void*)k_layer_norm_backward<DT, TAIL, 2, 512, 1, DROP>;
+            return (const void*)k_layer_norm_backward<DT, TAIL, 4, 512, false, DROP>;
+    return (const void*)k_layer_norm_backward<DT, TAIL, 2, 512, false, DROP>;
 }
 template <int DT>
 const void* backward_fn(const Spread& s, bool tail, bool drop)
@@ -507,6 +561,12 @@ hipError_t launch_layer_norm(const LayerNormArgs& in, int dtype, hipStream_t s)
     LayerNormArgs a = in;
     void* params[] = {&a};
     const size_t nvec = vectors(a.hidden, dtype);
+    if (nvec <= kWave) {   // several rows a workgroup
+        a.lanes = narrow_lanes(nvec);
+        const size_t per = 256 / (size_t)a.lanes;
+        return launch_logged("k_layer_norm", forward_of<1, 256, true>(dtype, partial(a.hidden, dtype)),
+                             dim3((unsigned)((a.rows + per - 1) / per)), dim3(256), params, s);
+    }
     const unsigned wg = forward_threads(nvec, a.rows);
     return launch_logged("k_layer_norm", forward_fn(dtype, partial(a.hidden, dtype), wg, nvec), dim3((unsigned)a.rows), dim3(wg),
                          params, s);
@@ -529,10 +589,11 @@ hipError_t launch_layer_norm_backward(const LayerNormBwdArgs& in, int dtype, hip
     a.parts = a.means + (2 * a.rows + 3) / 4 * 4;
     a.nparts = sp.parts;
     a.part_rows = sp.part_rows;
+    a.lanes = (int)sp.lanes;
     hipError_t e = hipSuccess;
     if (a.rows && sp.whole) {
         const void* fn = dtype == 0 ? backward_fn<0>(sp, tail, a.threshold) : backward_fn<1>(sp, tail, a.threshold);
-        e = launch_logged("k_layer_norm_backward", fn, dim3((unsigned)sp.parts), dim3(sp.threads * sp.teams), params, s);
+        e = launch_logged("k_layer_norm_backward", fn, dim3((unsigned)sp.parts), dim3(sp.threads), params, s);
     } else if (a.rows) {
         if (a.d_z) {
             const void* fn = dtype == 0 ? tail ? (const void*)k_layer_norm_means<0, true> : (const void*)k_layer_norm_means<0, false>
@@ -547,7 +608,7 @@ hipError_t launch_layer_norm_backward(const LayerNormBwdArgs& in, int dtype, hip
                                     : (const void*)k_layer_norm_columns<1, false>;
         e = launch_logged("k_layer_norm_columns", fn, dim3((unsigned)((nvec + kWave - 1) / kWave), (unsigned)sp.parts), dim3(256), params, s);
     }
-    if (e != hipSuccess || (!a.d_w && !a.d_b && !a.d_bias))
+    if (e != hipSuccess || (!a.d_w && !a.d_b && !a.d_bias) || (sp.whole && sp.parts == 1))
         return e;
     return launch_logged("k_layer_norm_params", (const void*)k_layer_norm_params, dim3((unsigned)((a.hidden + 63) / 64), 3), dim3(1024),
                          params, s);

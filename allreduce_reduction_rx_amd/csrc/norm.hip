@@ -40,7 +40,7 @@ __global__ __launch_bounds__(WG) void k_norm(NormArgs a)
         if (a.out_z) load(wpre, a.w_pre);
     }
     float y[NV][VE];
-    fold_row<DT, TAIL, NV>(a.src, a.nsrc, t * a.ld_src * EB, hidden, y);
+    fold_row<DT, TAIL, NV>(a.src, a.nsrc, t * a.ld_src * EB, hidden, tid, bd, y);
     if (a.w_post) {
         float s = 0.0f;
 #pragma unroll

@@ -62,13 +62,12 @@ __device__ __forceinline__ void fold_batch(const void* const* src, int r, size_t
 }
 
 // y = the sources' sum in their order, B sources' loads of a thread in flight
-// together.
+// together; thread `tid` of the `bd` that hold the row.
 template <int DT, bool TAIL, int NV>
-__device__ __forceinline__ void fold_row(const void* const* src, int nsrc, size_t row_bytes, int hidden,
+__device__ __forceinline__ void fold_row(const void* const* src, int nsrc, size_t row_bytes, int hidden, int tid, int bd,
                                          float (*y)[Elem<DT>::kVE])
 {
     constexpr int VE = Elem<DT>::kVE, B = NV == 1 ? 8 : 4;   // more would cost a longer row its occupancy
-    const int tid = (int)threadIdx.x, bd = (int)blockDim.x;
 #pragma unroll
     for (int u = 0; u < NV; ++u)
 #pragma unroll

@@ -12,25 +12,6 @@ namespace rx {
 namespace {
 
 
-template <int G>
-__device__ __forceinline__ float group_sum(float v)
-{
-    auto u = [](float x) { return __builtin_bit_cast(uint32_t, x); };
-    if constexpr (G >= 2) v += bits_f32(dpp<0xB1>(u(v)));
-    if constexpr (G >= 4) v += bits_f32(dpp<0x4E>(u(v)));
-    if constexpr (G >= 8) v += bits_f32(dpp<0x141>(u(v)));
-    if constexpr (G >= 16) v += bits_f32(dpp<0x140>(u(v)));
-    if constexpr (G >= 32) {
-        auto p = __builtin_amdgcn_permlane16_swap(u(v), u(v), false, false);
-        v = bits_f32(p[0]) + bits_f32(p[1]);
-    }
-    if constexpr (G >= 64) {
-        auto p = __builtin_amdgcn_permlane32_swap(u(v), u(v), false, false);
-        v = bits_f32(p[0]) + bits_f32(p[1]);
-    }
-    return v;
-}
-
 // Logits pos V .. pos V + V - 1 of a row: the loads, which wait for nothing, and
 // their values.
 template <int DT, int V> struct RawLogits { u32x4 v[V / Elem<DT>::kVE]; };
@@ -91,43 +72,6 @@ __device__ __forceinline__ float exp_of(float d)
 // each workgroup of the second launch.
 __device__ __host__ __forceinline__ size_t part_words(int experts) { return 2 * (size_t)experts; }
 constexpr int kSumExperts = 32;   // of a workgroup of the second launch
-
-// Sum over the lanes at this one's place in each group of G, the same in all.
-template <int G>
-__device__ __forceinline__ float across(float v)
-{
-    auto u = [](float x) { return __builtin_bit_cast(uint32_t, x); };
-    if constexpr (G <= 1) v += bits_f32(dpp<0x121>(u(v)));   // row_ror 1, 2, 4, 8
-    if constexpr (G <= 2) v += bits_f32(dpp<0x122>(u(v)));
-    if constexpr (G <= 4) v += bits_f32(dpp<0x124>(u(v)));
-    if constexpr (G <= 8) v += bits_f32(dpp<0x128>(u(v)));
-    if constexpr (G <= 16) {
-        auto p = __builtin_amdgcn_permlane16_swap(u(v), u(v), false, false);
-        v = bits_f32(p[0]) + bits_f32(p[1]);
-    }
-    if constexpr (G <= 32) {
-        auto p = __builtin_amdgcn_permlane32_swap(u(v), u(v), false, false);
-        v = bits_f32(p[0]) + bits_f32(p[1]);
-    }
-    return v;
-}
-template <int G>
-__device__ __forceinline__ uint32_t across(uint32_t v)
-{
-    if constexpr (G <= 1) v += dpp<0x121>(v);
-    if constexpr (G <= 2) v += dpp<0x122>(v);
-    if constexpr (G <= 4) v += dpp<0x124>(v);
-    if constexpr (G <= 8) v += dpp<0x128>(v);
-    if constexpr (G <= 16) {
-        auto p = __builtin_amdgcn_permlane16_swap(v, v, false, false);
-        v = p[0] + p[1];
-    }
-    if constexpr (G <= 32) {
-        auto p = __builtin_amdgcn_permlane32_swap(v, v, false, false);
-        v = p[0] + p[1];
-    }
-    return v;
-}
 
 // The losses from n tokens, the sum over the experts of count times sum of P,
 // and the sum of lse^2.

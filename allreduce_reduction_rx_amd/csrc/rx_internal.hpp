@@ -207,6 +207,7 @@ struct LayerNormArgs {
     uint32_t threshold;          // 65536 p; 0: no dropout
     float gain, eps, inv_hidden;
     int nsrc;
+    int lanes;                   // of a row, where a wave has several rows
 };
 
 struct LayerNormBwdArgs {
@@ -229,6 +230,7 @@ struct LayerNormBwdArgs {
     size_t part_rows, nparts;
     uint32_t threshold;
     float gain, inv_hidden;
+    int lanes;                   // of a row, where a workgroup has several rows
 };
 
 struct QuantFp4Args {

@@ -105,7 +105,7 @@ __device__ __forceinline__ Coded<GR> ld_coded(const uint8_t* brow, const float* 
     } else {
 #pragma unroll
         for (uint32_t i = 0; i < SG; ++i)
-            x.scale[i] = srow[g + i < groups ? g + i : groups - 1];
+            x.scale[i] = g + i < groups ? srow[g + i] : 0.0f;
     }
     return x;
 }
@@ -131,88 +131,227 @@ __device__ __forceinline__ void put4(const GemmFp4Args& a, const TileRows& rows,
 // group: exact products into a sum of the group's own, which the scale then
 // joins to acc. A row's scaling waits until the next row's products are on their
 // way. frag(r, m): the parts of row fragment r for the 32 of k number m.
-template <int DT, int GR, int TM, int TN, class F>
-__device__ __forceinline__ void multiply_chunk(const Coded<GR>* w, const F& frag, f32x4 (*acc)[TN])
+template <int DT, int GR, int TM, class F>
+__device__ __forceinline__ void multiply_chunk(const Coded<GR>& w, const F& frag, f32x4 (&acc)[TM])
 {
     constexpr int SG = 128 / GR, MG = 4 / SG;
-    u32x4 c[TN];
-#pragma unroll
-    for (int t = 0; t < TN; ++t)
-        c[t] = turned(w[t].codes);
+    const u32x4 c = turned(w.codes);
 #pragma unroll
     for (int g = 0; g < SG; ++g) {
-        bf16x8 b[MG][TN];
+        bf16x8 b[MG];
 #pragma unroll
         for (int m = 0; m < MG; ++m)
-#pragma unroll
-            for (int t = 0; t < TN; ++t)
-                b[m][t] = weights8(c[t][g * MG + m]);
-        f32x4 sum[2][TN];
+            b[m] = weights8(c[g * MG + m]);
+        f32x4 sum[2];
         auto scale = [&](int r) {
 #pragma unroll
-            for (int t = 0; t < TN; ++t)
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    acc[r][t][e] = __builtin_fmaf(sum[r & 1][t][e], w[t].scale[g], acc[r][t][e]);
+            for (int e = 0; e < 4; ++e)
+                acc[r][e] = __builtin_fmaf(sum[r & 1][e], w.scale[g], acc[r][e]);
         };
 #pragma unroll
         for (int r = 0; r < TM; ++r) {
-#pragma unroll
-            for (int t = 0; t < TN; ++t)
-                sum[r & 1][t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+            sum[r & 1] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
             for (int m = 0; m < MG; ++m) {
                 const Parts8<DT> x = frag(r, g * MG + m);
 #pragma unroll
                 for (int p = DT == 0 ? 2 : 0; p >= 0; --p)
-#pragma unroll
-                    for (int t = 0; t < TN; ++t)
-                        sum[r & 1][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x.p[p], b[m][t], sum[r & 1][t], 0, 0, 0);
+                    sum[r & 1] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x.p[p], b[m], sum[r & 1], 0, 0, 0);
             }
             if (r > 0)
                 scale(r - 1);
-            if (TM * TN >= 8)
-                __builtin_amdgcn_sched_barrier(0);   // more at once would not fit the registers
         }
         scale(TM - 1);
     }
 }
 
-// Few rows: 16 TT rows x 16 NS channels a workgroup of KS x NS waves, KC of k a
-// stage. Weights and scales go from memory to LDS without registers, each row's in one
-// piece, NBUF - 1 stages ahead; so do the rows of a where they are BF16 and whole
-// 16-byte units (WHOLE; TR of them), others go through registers one stage ahead, FP32
-// as its three parts, so that each element is taken apart once. A wave has 16
-// channels and every KS-th part of a stage; the KS sums meet in LDS in their order.
+__device__ __forceinline__ int wave_id() { return __builtin_amdgcn_readfirstlane((int)threadIdx.x / kWave); }
+
+// What rows of a and scales are past k: weights may be anything there, and 0 times
+// infinity is NaN.
+__device__ const u32x4 kNothing = {0, 0, 0, 0};
+
+// A stage of KC of k for BM rows of a and BN of b in LDS, and the loads that fill
+// it: weights and scales from memory to LDS without registers, each row's in one
+// piece; so do the rows of a where they are BF16 and whole 16-byte units (WHOLE; TR
+// of them), others go through registers, FP32 as its three parts, so that each
+// element is taken apart once.
 //
 // Why by way of LDS: a load of 64 lanes that takes 64 bytes from each of 16 rows
-// costs the cache 16 lines, as much as 2 KiB in one piece.
+// keeps the cache busy for 35 cycles, one that takes 128 bytes and more for 20 (30 and 50
+// bytes a cycle and CU), and 64 single words from as many lines for 65.
 //
 // Places in LDS: unit u (16 bytes) of row r sits where the sixteen rows of a read
 // lie in different banks; the load picks its unit to match. Rows that are not
 // there are not loaded, or are the last one again: their results are not used.
-template <int DT, int GR, int TT, int TR, int KS, int NS, int KC, int NBUF, bool WHOLE>
-__global__ __launch_bounds__(KS * NS * kWave) void k_gemm_fp4_stream(GemmFp4Args a)
-{
-    constexpr int EB = Elem<DT>::kBytes, BM = 16 * TT, BN = 16 * NS, kThreads = KS * NS * kWave;
-    constexpr int P = DT == 0 ? 3 : 1, UX = KC / 8, UW = KC / 32, SG = 128 / GR, SR = KC / GR;   // units of a row, scales a chunk and a row
-    constexpr int KW = KC / KS, kSteps = KW / 128;
-    constexpr int SU = SR % 4 == 0 && BN * SR % 256 == 0 ? 4 : 1;                                    // scales of a load
-    constexpr int kX = TR * UX, kW = BN * UW, kS = BN * SR;                        // units, units, scales of a stage
-    constexpr int NX = (kX + kThreads - 1) / kThreads, NW = (kW + kThreads - 1) / kThreads;
-    constexpr int NSC = (kS / SU + kThreads - 1) / kThreads, NS1 = (kS + kThreads - 1) / kThreads;
-    constexpr int N = (WHOLE ? NX : 0) + NW + NSC;
-    static_assert(KW % 128 == 0 && kX % kWave == 0 && kW % kWave == 0 && kS / SU % kWave == 0 && (NBUF == 2 || NBUF == 3), "");
-    static_assert((kX % kThreads == 0 || kX < kThreads) && (kW % kThreads == 0 || kW < kThreads) && (kS / SU % kThreads == 0 || kS / SU < kThreads), "");
-    struct Stage {
+template <int DT, int GR, int BM, int BN, int TR, int KC, int T, bool WHOLE>
+struct Stager {
+    static constexpr int EB = Elem<DT>::kBytes, P = DT == 0 ? 3 : 1;
+    static constexpr int UX = KC / 8, UW = KC / 32, SR = KC / GR;                 // units of a row, scales of a row
+    static constexpr int SU = SR % 4 == 0 && BN * SR % 256 == 0 ? 4 : 1;          // scales of a load
+    static constexpr int kX = TR * UX, kW = BN * UW, kS = BN * SR;                // units, units, scales of a stage
+    static constexpr int NX = WHOLE ? (kX + T - 1) / T : 0, NW = (kW + T - 1) / T;
+    static constexpr int NS = (kS / SU + T - 1) / T, NS1 = (kS + T - 1) / T;
+    static constexpr int N = NX + NW + NS;                                        // a thread's loads, at least
+    static constexpr int NXR = WHOLE ? 0 : (BM * UX + T - 1) / T;
+    static_assert(kX % kWave == 0 && kW % kWave == 0 && kS / SU % kWave == 0, "");
+    static_assert((kX % T == 0 || kX < T) && (kW % T == 0 || kW < T) && (kS / SU % T == 0 || kS / SU < T), "");
+    static_assert(WHOLE || ((UX >= kWave ? UX % kWave == 0 : kWave % UX == 0) && (BM * UX % T == 0 || BM * UX < T)), "");
+    struct Rows {
         u32x4 x[P][BM * UX];
+    };
+    struct Weights {
         u32x4 w[kW];
         float s[kS];
     };
-    __shared__ __align__(16) Stage ring[NBUF];
+    struct Stage : Rows, Weights {};
+
+    const char* xbase;
+    const uint8_t* wbase;
+    const float* sbase;
+    uint32_t last_row, last_col, ld_a, ld_b, groups, xunits, wunits;
+    int k, wave;
+    Raw8<DT> xreg[WHOLE ? 1 : NXR];
+
+    __device__ __forceinline__ Stager(const GemmFp4Args& a, const TileRows& rows, uint32_t n0)
+    {
+        k = (int)a.k;
+        wave = wave_id();
+        xunits = (uint32_t)k / 8;
+        wunits = (uint32_t)(k + 31) / 32;
+        xbase = static_cast<const char*>(a.a) + (size_t)rows.lo * a.ld_a * EB;
+        wbase = a.b + (size_t)rows.expert * a.stride_b + (size_t)n0 * a.ld_b;
+        sbase = a.b_scales + ((size_t)rows.expert * a.n + n0) * a.groups;
+        last_row = rows.hi - 1 - rows.lo;
+        last_col = a.n - 1 - n0;
+        ld_a = (uint32_t)a.ld_a * EB;   // below 2^25: 128 rows lie within 32 bits
+        ld_b = (uint32_t)a.ld_b;
+        groups = a.groups;
+    }
+    static __device__ __forceinline__ int wplace(int r, int u)
+    {
+        return u ^ (UW == 4 ? (r >> 2) & 3 : UW == 8 ? (r >> 1) & 7 : r & 15);
+    }
+    static __device__ __forceinline__ int splace(int r, int g) { return g ^ (r % 16 * SR / 64) / SU * SU; }
+    static __device__ __forceinline__ uint32_t least(uint32_t a, uint32_t b) { return a < b ? a : b; }
+
+    template <int B>
+    static __device__ __forceinline__ void copy(const void* from, void* to)   // the builtin wants a literal size
+    {
+        if constexpr (B == 16)
+            __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)from,
+                                             (__attribute__((address_space(3))) void*)to, 16, 0, 0);
+        else
+            __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)from,
+                                             (__attribute__((address_space(3))) void*)to, 4, 0, 0);
+    }
+    template <int U>
+    __device__ __forceinline__ void load_scales(int st, Weights& to, int i) const
+    {
+        const int e = (i * T + (int)threadIdx.x) % (kS / U), r = e * U / SR;
+        const uint32_t g = (uint32_t)(st * SR + splace(r, e * U % SR));
+        const float* from = sbase + (least((uint32_t)r, last_col) * groups + g);
+        copy<4 * U>(g < groups ? from : (const float*)&kNothing, &to.s[(i * T + wave * kWave) % (kS / U) * U]);
+    }
+    // Load I of stage st. Weights past k: the row's first ones, which zeros meet.
+    template <int I, class To>
+    __device__ __forceinline__ void load(int st, To& to) const
+    {
+        const int tid = (int)threadIdx.x;
+        if constexpr (I < NX) {
+            const int e = (I * T + tid) % kX, r = e / UX;
+            const uint32_t u = (uint32_t)(st * UX + (e % UX ^ (r & 15)));
+            const char* from = xbase + (least((uint32_t)r, last_row) * ld_a + u * 16);
+            copy<16>(u < xunits ? from : (const char*)&kNothing, &to.x[0][(I * T + wave * kWave) % kX]);
+        } else if constexpr (I < NX + NW) {
+            constexpr int i = I - NX;
+            const int e = (i * T + tid) % kW, r = e / UW;
+            const uint32_t u = (uint32_t)(st * UW + wplace(r, e % UW));
+            copy<16>(wbase + (least((uint32_t)r, last_col) * ld_b + (u < wunits ? u : 0) * 16), &to.w[(i * T + wave * kWave) % kW]);
+        } else if constexpr (I < N) {
+            // four scales at a time, one at a time where the row ends in the stage
+            constexpr int i = I - NX - NW;
+            if (SU > 1 && (uint32_t)(st + 1) * SR <= groups) {
+                load_scales<SU>(st, to, i);
+            } else {
+#pragma unroll
+                for (int j = i * NS1 / NS; j < (i + 1) * NS1 / NS; ++j)
+                    load_scales<1>(st, to, j);
+            }
+        }
+    }
+    // The rows that go through registers: a stage's loads, asked for before the
+    // stage's other loads, so that the wait for those need not count them.
+    template <int I>
+    __device__ __forceinline__ void load_x(int st)
+    {
+        if constexpr (I < NXR) {
+            const uint32_t e = (uint32_t)(I * T) + threadIdx.x, r = e / UX;
+            if (r <= last_row && r < BM) {
+                const char* row = xbase + r * ld_a;
+                const int at = st * KC + (int)(e % UX) * 8;
+                xreg[I] = (st + 1) * KC <= k ? ld_raw8<DT, false>(row, at, k) : ld_raw8<DT, true>(row, at, k);
+            }
+        }
+    }
+    __device__ __forceinline__ void store_x(Rows& to)
+    {
+        if constexpr (NXR > 0)
+#pragma unroll
+            for (int i = 0; i < NXR; ++i) {
+                const uint32_t e = (uint32_t)(i * T) + threadIdx.x, r = e / UX;
+                if (r <= last_row && r < BM) {
+                    const Parts8<DT> x = parts8<DT>(xreg[i]);
+#pragma unroll
+                    for (int p = 0; p < P; ++p)
+                        to.x[p][r * UX + (e % UX ^ (r & 15))] = __builtin_bit_cast(u32x4, x.p[p]);
+                }
+            }
+    }
+    // Eight elements of row r (r % 16 = lane % 16) from k0 of the stage on.
+    static __device__ __forceinline__ Parts8<DT> rows_of(const Rows& st, int r, int k0)
+    {
+        Parts8<DT> f;
+#pragma unroll
+        for (int p = 0; p < P; ++p)
+            f.p[p] = __builtin_bit_cast(bf16x8, st.x[p][r * UX + (k0 / 8 ^ (r & 15))]);
+        return f;
+    }
+    // Dword q of unit m of weight row r.
+    static __device__ __forceinline__ uint32_t codes_of(const Weights& st, int r, int m, int q)
+    {
+        return reinterpret_cast<const uint32_t*>(&st.w[r * UW + wplace(r, m)])[q];
+    }
+    static __device__ __forceinline__ float scale_of(const Weights& st, int r, int g) { return st.s[r * SR + splace(r, g)]; }
+};
+
+// Waits for a stage's loads and the waves: the stage is there, and the one
+// before has been read. `next`: N loads of a later stage may still be on their way.
+template <int N>
+__device__ __forceinline__ void open_stage(bool next)
+{
+    if (N > 0 && next)
+        wait_loads<N>();
+    else
+        wait_loads<0>();
+    wait_lds();
+    order();
+    __builtin_amdgcn_s_barrier();
+    order();
+}
+
+// Few rows: 16 TT rows x 16 NS channels a workgroup of KS x NS waves, KC of k a
+// stage, NBUF - 1 stages on their way. A wave has 16 channels and every KS-th part of a
+// stage; the KS sums meet in LDS in their order.
+template <int DT, int GR, int TT, int TR, int KS, int NS, int KC, int NBUF, bool WHOLE>
+__global__ __launch_bounds__(KS * NS * kWave) void k_gemm_fp4_stream(GemmFp4Args a)
+{
+    constexpr int BM = 16 * TT, BN = 16 * NS, SG = 128 / GR, KW = KC / KS;
+    using S = Stager<DT, GR, BM, BN, TR, KC, KS * NS * kWave, WHOLE>;
+    static_assert(KW % 128 == 0 && (NBUF == 2 || NBUF == 3), "");
+    __shared__ __align__(16) typename S::Stage ring[NBUF];
     static_assert(sizeof(ring) >= sizeof(f32x4) * KS * NS * TT * kWave && sizeof(ring) <= 160 * 1024, "");
-    const int tid = threadIdx.x, lane = lane_id(), wave = __builtin_amdgcn_readfirstlane(tid / kWave);
-    const int ks = wave % KS, ns = wave / KS, col = lane % 16, q = lane / 16;
+    const int lane = lane_id(), wave = wave_id(), ks = wave % KS, ns = wave / KS, col = lane % 16, q = lane / 16;
     const Tiles tiles = count_tiles(a, BM);
     uint32_t tm, tn;
     if (!pick_tile(tiles, (a.n + BN - 1) / BN, tm, tn))
@@ -225,153 +364,45 @@ __global__ __launch_bounds__(KS * NS * kWave) void k_gemm_fp4_stream(GemmFp4Args
         zero_tile<DT>(a, rows, n0, BN);
         return;
     }
+    S s(a, rows, n0);
     const int k = (int)a.k, stages = (k + KC - 1) / KC;
-    const uint32_t xunits = (uint32_t)k / 8, wunits = (uint32_t)(k + 31) / 32;
-    const char* xbase = static_cast<const char*>(a.a) + (size_t)rows.lo * a.ld_a * EB;
-    const uint8_t* wbase = a.b + (size_t)rows.expert * a.stride_b + (size_t)n0 * a.ld_b;
-    const float* sbase = a.b_scales + ((size_t)rows.expert * a.n + n0) * a.groups;
-    const uint32_t last_row = rows.hi - 1 - rows.lo, last_col = a.n - 1 - n0;
-    auto wplace = [](int r, int u) { return u ^ (UW == 4 ? (r >> 2) & 3 : UW == 8 ? (r >> 1) & 7 : r & 15); };
-    // scales of a row in units of SU
-    auto splace = [](int r, int g) { return g ^ (r % 16 * SR / 64) / SU * SU; };
-    // what this thread loads: below 2^32, 64 rows of a stride below 2^23 elements
-    uint32_t xfrom[NX], xunit[NX], wfrom[NW], wunit[NW];
+    f32x4 acc[TT] = {};
+    // this wave's part of a stage
+    auto multiply = [&](const typename S::Stage& st, int left) {
 #pragma unroll
-    for (int i = 0; i < NX; ++i) {
-        const int e = (i * kThreads + tid) % kX, r = e / UX;
-        xfrom[i] = ((uint32_t)r < last_row ? (uint32_t)r : last_row) * (uint32_t)a.ld_a * EB;
-        xunit[i] = (uint32_t)(e % UX ^ (r & 15));
-    }
-#pragma unroll
-    for (int i = 0; i < NW; ++i) {
-        const int e = (i * kThreads + tid) % kW, r = e / UW;
-        wfrom[i] = ((uint32_t)r < last_col ? (uint32_t)r : last_col) * (uint32_t)a.ld_b;
-        wunit[i] = (uint32_t)wplace(r, e % UW);
-    }
-    // past k: the row's first unit, which nothing reads or zeros meet
-    auto load = [&](int st, int buf) {
-        Stage& to = ring[buf];
-        if constexpr (WHOLE)
-#pragma unroll
-            for (int i = 0; i < NX; ++i) {
-                const uint32_t u = (uint32_t)st * UX + xunit[i];
-                __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)(xbase + (xfrom[i] + (u < xunits ? u : 0) * 16)),
-                                                 (__attribute__((address_space(3))) void*)&to.x[0][(i * kThreads + wave * kWave) % kX], 16, 0, 0);
-            }
-#pragma unroll
-        for (int i = 0; i < NW; ++i) {
-            const uint32_t u = (uint32_t)st * UW + wunit[i];
-            __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)(wbase + (wfrom[i] + (u < wunits ? u : 0) * 16)),
-                                             (__attribute__((address_space(3))) void*)&to.w[(i * kThreads + wave * kWave) % kW], 16, 0, 0);
-        }
-        // scales: four at a time, one at a time where the row ends in the stage
-        auto load_s = [&](auto count, auto each) {
-            constexpr int U = each();
-#pragma unroll
-            for (int i = 0; i < count(); ++i) {
-                const int e = (i * kThreads + tid) % (kS / U), r = e * U / SR;
-                const uint32_t g = (uint32_t)(st * SR + splace(r, e * U % SR)), row = (uint32_t)r < last_col ? (uint32_t)r : last_col;
-                auto from = (const __attribute__((address_space(1))) void*)(sbase + (row * a.groups + (g < a.groups ? g : 0)));
-                auto at = (__attribute__((address_space(3))) void*)&to.s[(i * kThreads + wave * kWave) % (kS / U) * U];
-                if constexpr (U == 4)
-                    __builtin_amdgcn_global_load_lds(from, at, 16, 0, 0);
-                else
-                    __builtin_amdgcn_global_load_lds(from, at, 4, 0, 0);
-            }
-        };
-        using std::integral_constant;
-        if (SU > 1 && (uint32_t)(st + 1) * SR <= a.groups)
-            load_s(integral_constant<int, NSC>(), integral_constant<int, SU>());
-        else
-            load_s(integral_constant<int, NS1>(), integral_constant<int, 1>());
-    };
-    // ... through registers: one stage ahead, asked for before the stage's other loads,
-    // so that the wait for those need not count them
-    constexpr int NXR = (BM * UX + kThreads - 1) / kThreads;
-    static_assert(WHOLE || ((UX >= kWave ? UX % kWave == 0 : kWave % UX == 0) && (BM * UX % kThreads == 0 || BM * UX < kThreads)), "");
-    Raw8<DT> xreg[WHOLE ? 1 : NXR];
-    auto load_x = [&](int st) {
-#pragma unroll
-        for (int i = 0; i < NXR; ++i) {
-            const uint32_t e = (uint32_t)(i * kThreads + tid), r = e / UX;
-            if (r <= last_row && r < BM) {
-                const char* row = xbase + r * (uint32_t)a.ld_a * EB;
-                const int at = st * KC + (int)(e % UX) * 8;
-                xreg[WHOLE ? 0 : i] = (st + 1) * KC <= k ? ld_raw8<DT, false>(row, at, k) : ld_raw8<DT, true>(row, at, k);
-            }
-        }
-    };
-    auto store_x = [&](int buf) {
-#pragma unroll
-        for (int i = 0; i < NXR; ++i) {
-            const uint32_t e = (uint32_t)(i * kThreads + tid), r = e / UX;
-            if (r <= last_row && r < BM) {
-                const Parts8<DT> x = parts8<DT>(xreg[WHOLE ? 0 : i]);
-#pragma unroll
-                for (int p = 0; p < P; ++p)
-                    ring[buf].x[p][r * UX + (e % UX ^ (r & 15))] = __builtin_bit_cast(u32x4, x.p[p]);
-            }
-        }
-    };
-    f32x4 acc[TT][1] = {};
-    // chunk j of this wave's part of a stage; PART: k ends in the stage
-    auto multiply = [&](const Stage& st, int left, auto part) {
-#pragma unroll
-        for (int j = 0; j < kSteps; ++j) {
+        for (int j = 0; j < KW / 128; ++j) {
             const int k0 = ks * KW + j * 128;
-            if (part() && k0 >= left)
+            if (k0 >= left)
                 break;
             const int r = ns * 16 + col;
-            Coded<GR> w[1];
-            w[0].codes = st.w[r * UW + wplace(r, k0 / 32 + q)];
+            Coded<GR> w;
+            w.codes = st.w[r * S::UW + S::wplace(r, k0 / 32 + q)];
 #pragma unroll
             for (int g = 0; g < SG; ++g)
-                w[0].scale[g] = st.s[r * SR + splace(r, k0 / GR + g)];
-            multiply_chunk<DT, GR, TT, 1>(w, [&](int t, int m) {
-                Parts8<DT> f;
-#pragma unroll
-                for (int p = 0; p < P; ++p) {
-                    u32x4 x = st.x[p][(t * 16 + col) * UX + ((k0 / 8 + m * 4 + q) ^ col)];
-                    if (WHOLE && part()) {
-                        const int in = left - (k0 + m * 32 + q * 8);   // elements before k's end: all or none
-#pragma unroll
-                        for (int d = 0; d < 4; ++d)
-                            x[d] = in > 0 ? x[d] : 0;
-                    }
-                    f.p[p] = __builtin_bit_cast(bf16x8, x);
-                }
-                return f;
-            }, acc);
+                w.scale[g] = S::scale_of(st, r, k0 / GR + g);
+            multiply_chunk<DT, GR, TT>(w, [&](int t, int m) { return S::rows_of(st, t * 16 + col, k0 + m * 32 + q * 8); }, acc);
         }
     };
-    if (!WHOLE && stages > 0)
+    auto load_x = [&](int st) {
+        unrolled<S::NXR>([&](auto i) { s.template load_x<i()>(st); });
+        order();
+    };
+    auto load = [&](int st, int buf) { unrolled<S::N>([&](auto i) { s.template load<i()>(st, ring[buf]); }); };
+    if (S::NXR > 0 && stages > 0)
         load_x(0);
-    order();
 #pragma unroll
     for (int st = 0; st < NBUF - 1; ++st)
         if (st < stages)
             load(st, st);
     int buf = 0;
     for (int st = 0; st < stages; ++st) {
-        if constexpr (!WHOLE)
-            store_x(buf);
-        if (NBUF > 2 && st + 1 < stages)
-            wait_loads<(NBUF - 2) * N>();   // the next stage's, which are behind this one's
-        else
-            wait_loads<0>();
-        wait_lds();
-        order();
-        __builtin_amdgcn_s_barrier();   // this stage is there, and the one before is read
-        order();
-        if (!WHOLE && st + 1 < stages)
+        s.store_x(ring[buf]);
+        open_stage<(NBUF - 2) * S::N>(st + 1 < stages);
+        if (S::NXR > 0 && st + 1 < stages)
             load_x(st + 1);
-        order();
         if (st + NBUF - 1 < stages)
             load(st + NBUF - 1, buf == 0 ? NBUF - 1 : buf - 1);
-        if ((st + 1) * KC <= k)
-            multiply(ring[buf], KC, std::integral_constant<bool, false>());
-        else
-            multiply(ring[buf], k - st * KC, std::integral_constant<bool, true>());
+        multiply(ring[buf], k - st * KC);
         buf = buf + 1 == NBUF ? 0 : buf + 1;
     }
     auto put = [&](int t, int group, f32x4 v) {
@@ -380,13 +411,13 @@ __global__ __launch_bounds__(KS * NS * kWave) void k_gemm_fp4_stream(GemmFp4Args
     if constexpr (KS == 1) {
 #pragma unroll
         for (int t = 0; t < TT; ++t)
-            put(t, ns, acc[t][0]);
+            put(t, ns, acc[t]);
     } else {
         f32x4* joined = reinterpret_cast<f32x4*>(&ring[0]);
         __syncthreads();
 #pragma unroll
         for (int t = 0; t < TT; ++t)
-            joined[((ns * TT + t) * KS + ks) * kWave + lane] = acc[t][0];
+            joined[((ns * TT + t) * KS + ks) * kWave + lane] = acc[t];
         __syncthreads();
         for (int i = wave; i < NS * TT; i += KS * NS) {
             f32x4 v = joined[i * KS * kWave + lane];
@@ -430,16 +461,16 @@ __global__ __launch_bounds__(8 * kWave) void k_gemm_fp4_few(GemmFp4Args a)
     const char* xat = static_cast<const char*>(a.a) + ((size_t)rows.lo + xrow) * a.ld_a * EB;
     const uint8_t* bat = a.b + (size_t)rows.expert * a.stride_b + (size_t)(n0 + brow) * a.ld_b;
     const float* sat = a.b_scales + ((size_t)rows.expert * a.n + n0 + brow) * a.groups;
-    Coded<GR> w[D][1];
+    Coded<GR> w[D];
     Raw8<DT> xs[D][4];
     auto load = [&](int i, int d) {
         const int at = ks + i * KS, k0 = at * 128 + q * 8;
 #pragma unroll
         for (int s = 0; s < 4; ++s)
             xs[d][s] = at * 128 + 128 <= k ? ld_raw8<DT, false>(xat, k0 + 32 * s, k) : ld_raw8<DT, true>(xat, k0 + 32 * s, k);
-        w[d][0] = ld_coded<GR>(bat, sat, (uint32_t)at, kbytes, a.groups);
+        w[d] = ld_coded<GR>(bat, sat, (uint32_t)at, kbytes, a.groups);
     };
-    f32x4 acc[1][1] = {};
+    f32x4 acc[1] = {};
 #pragma unroll
     for (int d = 0; d < D; ++d)
         if (d < mine)
@@ -449,12 +480,12 @@ __global__ __launch_bounds__(8 * kWave) void k_gemm_fp4_few(GemmFp4Args a)
         for (int d = 0; d < D; ++d) {
             if (i + d >= mine)
                 break;
-            multiply_chunk<DT, GR, 1, 1>(w[d], [&](int, int m) { return parts8<DT>(xs[d][m]); }, acc);
+            multiply_chunk<DT, GR, 1>(w[d], [&](int, int m) { return parts8<DT>(xs[d][m]); }, acc);
             if (i + d + D < mine)
                 load(i + d + D, d);
         }
     }
-    joined[ks][lane] = acc[0][0];
+    joined[ks][lane] = acc[0];
     __syncthreads();
     if (ks == 0) {
         f32x4 v = joined[0][lane];
@@ -465,22 +496,143 @@ __global__ __launch_bounds__(8 * kWave) void k_gemm_fp4_few(GemmFp4Args a)
     }
 }
 
-// Many rows: BM x BN results a workgroup of WM x WN waves, TM x TN products of 16 x
-// 16 each. The rows' chunk of 128 of k is in LDS (FP32 as its three parts), the
-// next one on its way there; the weights go to registers, and to BF16 by every
-// wave that needs them, while the matrix cores run. Unit u of 8 elements of
-// row r sits at u ^ r % 16, so that the sixteen rows of a read lie in different
-// banks. DIRECT: BF16 rows that start 16-byte aligned go to LDS without
-// registers; others, and a chunk that k ends in, through them.
-template <int DT, int GR, int TM, int TN, int WM, int WN, bool DIRECT>
-__global__ __launch_bounds__(WM * WN * kWave, 2) void k_gemm_fp4_tile(GemmFp4Args a)
+// Here, not later: the compiler would move sums to where they are next used, past the
+// branches between, and hold all that they are made of until then.
+template <int N>
+__device__ __forceinline__ void keep(f32x4 (&x)[N])
 {
-    constexpr int BM = 16 * TM * WM, BN = 16 * TN * WN, EB = Elem<DT>::kBytes, P = DT == 0 ? 3 : 1;
-    constexpr int kThreads = WM * WN * kWave, kRowsAPass = kThreads / 16, NP = BM / kRowsAPass, NBUF = DT == 0 ? 1 : 2;
-    static_assert(BM % kRowsAPass == 0 && kRowsAPass % 16 == 0, "");
-    __shared__ u32x4 xs[NBUF][P][BM][16];
-    const int tid = threadIdx.x, lane = lane_id(), wave = __builtin_amdgcn_readfirstlane(tid / kWave);
-    const int col = lane % 16, q = lane / 16;
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+        asm volatile("" : "+v"(x[i]));
+}
+
+// Many BF16 rows: 128 x 256 results a workgroup of 2 x 4 waves, one on a CU, 4 x 4
+// products of 16 x 16 a wave, 128 of k a stage, one or two stages on their way. Steps of one
+// row fragment: its products, and while the matrix cores run the fragment after
+// the next is read, the next 32's weights are made (their values are exact in BF16),
+// the scales join the sums of the step before, and a later stage asks for its share:
+// all loads at once would hold the wave up for as long as the cache takes them. A stage
+// is opened before the one before has ended, so that its first steps find their operands.
+template <int GR>
+__global__ __launch_bounds__(8 * kWave, 2) void k_gemm_fp4_tile(GemmFp4Args a)
+{
+    constexpr int TM = 4, TN = 4, WM = 2, WN = 4, NBUF = 3, KC = 128;
+    constexpr int BM = 16 * TM * WM, BN = 16 * TN * WN, MG = GR / 32, SG = 4 / MG, kSteps = 4 * TM;
+    using S = Stager<1, GR, BM, BN, BM, KC, WM * WN * kWave, true>;
+    constexpr int kOpen = kSteps - S::N;   // the first step that may read the next stage
+    static_assert(kOpen >= 0 && kOpen <= 2 * TM + TM - 1, "");
+    __shared__ __align__(16) typename S::Stage ring[NBUF];
+    static_assert(sizeof(ring) <= 160 * 1024, "");
+    const int lane = lane_id(), wave = wave_id(), col = lane % 16, q = lane / 16;
+    const Tiles tiles = count_tiles(a, BM);
+    uint32_t tm, tn;
+    if (!pick_tile(tiles, (a.n + BN - 1) / BN, tm, tn))
+        return;
+    const uint32_t n0 = tn * BN;
+    const TileRows rows = find_tile(a, tiles, tm, BM);
+    if (rows.lo >= rows.hi)
+        return;
+    if (rows.expert < 0) {
+        zero_tile<1>(a, rows, n0, BN);
+        return;
+    }
+    S s(a, rows, n0);
+    const int stages = ((int)a.k + KC - 1) / KC;
+    const int wm = wave / WN * TM * 16, wn = wave % WN * TN * 16;
+    f32x4 acc[TM][TN] = {}, sum[TM][TN] = {};
+    uint32_t code[2][TN];
+    float by[2][TN] = {};
+    bf16x8 b[2][TN], f[4];
+    auto row = [&](int t) { return wn + t * 16 + col; };
+    auto frag = [&](const typename S::Stage& st, int n) { return S::rows_of(st, wm + n % TM * 16 + col, n / TM * 32 + q * 8).p[0]; };
+    auto scale = [&](int r) {
+#pragma unroll
+        for (int t = 0; t < TN; ++t)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                acc[r][t][e] = __builtin_fmaf(sum[r][t][e], by[0][t], acc[r][t][e]);
+        keep(acc[r]);
+    };
+    if (stages > 0) {
+        unrolled<S::N>([&](auto i) { s.template load<i()>(0, ring[0]); });
+        if (stages > 1)
+            unrolled<S::N>([&](auto i) { s.template load<i()>(1, ring[1]); });
+        open_stage<S::N>(stages > 1);
+        f[0] = frag(ring[0], 0);
+        f[1] = frag(ring[0], 1);
+#pragma unroll
+        for (int t = 0; t < TN; ++t) {
+            code[0][t] = S::codes_of(ring[0], row(t), 0, q);
+            code[1][t] = S::codes_of(ring[0], row(t), 1, q);
+            by[1][t] = S::scale_of(ring[0], row(t), 0);
+            b[0][t] = weights8(code[0][t]);
+        }
+    }
+    int buf = 0;
+    for (int st = 0; st < stages; ++st) {
+        const typename S::Stage& now = ring[buf];
+        buf = buf + 1 == NBUF ? 0 : buf + 1;
+        const typename S::Stage& then = ring[buf];   // past the last one: anything, for nothing
+        typename S::Stage& late = ring[buf + 1 == NBUF ? 0 : buf + 1];
+        unrolled<kSteps>([&](auto step) {
+            constexpr int n = step(), m = n / TM, r = n % TM, before = (n + kSteps - 1) % kSteps;   // before: its products are done
+            if constexpr (n == kOpen)   // nothing but the next stage is on its way
+                open_stage<0>(false);
+            f[(n + 2) % 4] = n + 2 < kSteps ? frag(now, n + 2) : frag(then, n + 2 - kSteps);
+#pragma unroll
+            for (int t = 0; t < TN; ++t)
+                sum[r][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(f[n % 4], b[m & 1][t],
+                                                                    m % MG == 0 ? f32x4{0.0f, 0.0f, 0.0f, 0.0f} : sum[r][t], 0, 0, 0);
+            if constexpr (n >= kOpen)
+                if (st + 2 < stages)
+                    s.template load<n - kOpen>(st + 2, late);
+            if constexpr (before / TM % MG == MG - 1)
+                scale(before % TM);
+            // a share of the next weights
+#pragma unroll
+            for (int t = r * TN / TM; t < (r + 1) * TN / TM; ++t)
+                b[(m + 1) & 1][t] = weights8(code[(m + 1) & 1][t]);
+            if constexpr (r == TM - 1)
+#pragma unroll
+                for (int t = 0; t < TN; ++t)
+                    code[m & 1][t] = m < 2 ? S::codes_of(now, row(t), m + 2, q) : S::codes_of(then, row(t), m - 2, q);
+            if constexpr (r == 0 && m % MG == 0)   // the scales before have joined
+#pragma unroll
+                for (int t = 0; t < TN; ++t) {
+                    by[0][t] = by[1][t];
+                    if (m / MG + 1 < SG)
+                        by[1][t] = S::scale_of(now, row(t), m / MG + 1);
+                }
+            if constexpr (n == kSteps - 3)
+#pragma unroll
+                for (int t = 0; t < TN; ++t)
+                    by[1][t] = S::scale_of(then, row(t), 0);
+            __builtin_amdgcn_sched_barrier(0);
+        });
+    }
+    scale(TM - 1);
+#pragma unroll
+    for (int r = 0; r < TM; ++r)
+#pragma unroll
+        for (int t = 0; t < TN; ++t)
+            put4<1>(a, rows, rows.lo + (uint32_t)(wm + r * 16 + q * 4), n0 + (uint32_t)(wn + t * 16 + col), acc[r][t]);
+}
+
+// Many FP32 rows: 64 x 128 results a workgroup of 2 x 2 waves, two on a CU, 2 x 4 products of
+// 16 x 16 a wave (four channels to a fragment of three parts: with two, LDS would
+// be as busy as the matrix cores), 128 of k a stage. The rows have one place in LDS and
+// the next stage's wait in registers; the other workgroup computes while this one
+// changes stages. 512 x 8192 x 8192: 190 us, three products at 1.08 PFLOP/s.
+template <int GR>
+__global__ __launch_bounds__(4 * kWave, 2) void k_gemm_fp4_parts(GemmFp4Args a)
+{
+    constexpr int DT = 0, TM = 2, TN = 4, WM = 2, WN = 2, KC = 128;
+    constexpr int BM = 16 * TM * WM, BN = 16 * TN * WN, MG = GR / 32, P = 3, kSteps = 4 * TM;
+    using S = Stager<DT, GR, BM, BN, BM, KC, WM * WN * kWave, false>;
+    __shared__ __align__(16) typename S::Rows x;
+    __shared__ __align__(16) typename S::Weights ring[2];
+    static_assert(S::NXR + S::N <= kSteps && sizeof(x) + sizeof(ring) <= 80 * 1024, "");
+    const int lane = lane_id(), wave = wave_id(), col = lane % 16, q = lane / 16;
     const Tiles tiles = count_tiles(a, BM);
     uint32_t tm, tn;
     if (!pick_tile(tiles, (a.n + BN - 1) / BN, tm, tn))
@@ -493,132 +645,88 @@ __global__ __launch_bounds__(WM * WN * kWave, 2) void k_gemm_fp4_tile(GemmFp4Arg
         zero_tile<DT>(a, rows, n0, BN);
         return;
     }
-    const int k = (int)a.k, chunks = (k + 127) / 128;
-    const uint32_t kbytes = (uint32_t)(k + 31) / 32 * 16;
-    const char* xbase = static_cast<const char*>(a.a) + (size_t)rows.lo * a.ld_a * EB;
-    const uint8_t* bbase = a.b + (size_t)rows.expert * a.stride_b + (size_t)n0 * a.ld_b;
-    const float* sbase = a.b_scales + ((size_t)rows.expert * a.n + n0) * a.groups;
+    S s(a, rows, n0);
+    const int stages = ((int)a.k + KC - 1) / KC;
     const int wm = wave / WN * TM * 16, wn = wave % WN * TN * 16;
-    const int xr = tid / 16, xu = tid % 16;   // this thread's row and unit of a pass
-    const uint32_t last_row = rows.hi - 1 - rows.lo, last_col = a.n - 1 - n0;
-    auto row_at = [&](int i) {   // of pass i, in bytes below 2^32
-        const uint32_t r = (uint32_t)(i * kRowsAPass + xr);
-        return (r < last_row ? r : last_row) * (uint32_t)a.ld_a * EB;
-    };
-    uint32_t bfrom[TN], sfrom[TN];
-#pragma unroll
-    for (int i = 0; i < TN; ++i) {
-        const uint32_t r = (uint32_t)(wn + i * 16 + col), at = r < last_col ? r : last_col;
-        bfrom[i] = at * (uint32_t)a.ld_b;
-        sfrom[i] = at * a.groups;
-    }
-    Coded<GR> w[2][TN];
-    auto load_w = [&](int c, Coded<GR>* to) {
-#pragma unroll
-        for (int t = 0; t < TN; ++t)
-            to[t] = ld_coded<GR>(bbase + bfrom[t], sbase + sfrom[t], (uint32_t)c, kbytes, a.groups);
-    };
-    auto store_x = [&](int buf, int i, const Raw8<DT>& x) {
-        const Parts8<DT> p = parts8<DT>(x);
-#pragma unroll
-        for (int j = 0; j < P; ++j)
-            xs[buf][j][i * kRowsAPass + xr][xu ^ (xr & 15)] = __builtin_bit_cast(u32x4, p.p[j]);
-    };
+    auto row = [&](int t) { return wn + t * 16 + col; };
     f32x4 acc[TM][TN] = {};
-    int buf = 0;
-    auto frag = [&](int r, int m) {
-        Parts8<DT> f;
+    if (stages > 0) {
+        unrolled<S::NXR>([&](auto i) { s.template load_x<i()>(0); });
+        order();
+        unrolled<S::N>([&](auto i) { s.template load<i()>(0, ring[0]); });
+    }
+    for (int st = 0; st < stages; ++st) {
+        const typename S::Weights& now = ring[st & 1];
+        typename S::Weights& late = ring[st & 1 ^ 1];
+        order();
+        __builtin_amdgcn_s_barrier();   // the stage before has been read
+        order();
+        s.store_x(x);
+        open_stage<0>(false);
+        uint32_t code[2][TN];
+        float by[2][TN];
+        bf16x8 b[2][TN];
+        f32x4 sum[TM][TN];
+        Parts8<DT> f[3];
+        auto frag = [&](int n) { return S::rows_of(x, wm + n % TM * 16 + col, n / TM * 32 + q * 8); };
+        auto scale = [&](int r, int g) {
 #pragma unroll
-        for (int p = 0; p < P; ++p)
-            f.p[p] = __builtin_bit_cast(bf16x8, xs[buf][p][wm + r * 16 + col][(m * 4 + q) ^ col]);
-        return f;
-    };
-    if constexpr (DT == 1) {
-        auto load_x = [&](int c, int to) {
-            if (DIRECT && c * 128 + 128 <= k) {
-                // LDS is written in lane order: the lane picks the unit that belongs there
+            for (int t = 0; t < TN; ++t)
 #pragma unroll
-                for (int i = 0; i < NP; ++i)
-                    __builtin_amdgcn_global_load_lds(
-                        (const __attribute__((address_space(1))) void*)(xbase + (row_at(i) + (uint32_t)(c * 256 + (xu ^ (xr & 15)) * 16))),
-                        (__attribute__((address_space(3))) void*)&xs[to][0][i * kRowsAPass + wave * 4][0], 16, 0, 0);
-            } else {
-#pragma unroll 1
-                for (int i = 0; i < NP; i += 4) {
-                    Raw8<DT> x[4];
-#pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        x[j] = ld_raw8<DT, true>(xbase + row_at(i + j), c * 128 + xu * 8, k);
-#pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        store_x(to, i + j, x[j]);
-                }
-            }
+                for (int e = 0; e < 4; ++e)
+                    acc[r][t][e] = __builtin_fmaf(sum[r][t][e], by[g & 1][t], acc[r][t][e]);
+            keep(acc[r]);
         };
-        static_assert(NP % 4 == 0, "");
-        if (chunks > 0) {
-            load_x(0, 0);
-            load_w(0, w[0]);
-        }
-        for (int c = 0; c < chunks; c += 2) {
+        f[0] = frag(0);
+        f[1] = frag(1);
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                if (c + h >= chunks)
-                    break;
-                // this chunk has arrived, and every wave is done with the one before
-                wait_loads<0>();
-                wait_lds();
-                order();
-                __builtin_amdgcn_s_barrier();
-                order();
-                if (c + h + 1 < chunks) {
-                    load_x(c + h + 1, h ^ 1);
-                    load_w(c + h + 1, w[h ^ 1]);
+        for (int t = 0; t < TN; ++t) {
+            code[0][t] = S::codes_of(now, row(t), 0, q);
+            code[1][t] = S::codes_of(now, row(t), 1, q);
+            by[0][t] = S::scale_of(now, row(t), 0);
+            b[0][t] = weights8(code[0][t]);
+        }
+        unrolled<kSteps>([&](auto step) {
+            constexpr int n = step(), m = n / TM, r = n % TM, before = n - 1;   // before: its products are done
+            if constexpr (n + 2 < kSteps)
+                f[(n + 2) % 3] = frag(n + 2);
+#pragma unroll
+            for (int p = P - 1; p >= 0; --p)
+#pragma unroll
+                for (int t = 0; t < TN; ++t) {
+                    const bool first = m % MG == 0 && p == P - 1;
+                    sum[r][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(f[n % 3].p[p], b[m & 1][t],
+                                                                        first ? f32x4{0.0f, 0.0f, 0.0f, 0.0f} : sum[r][t], 0, 0, 0);
                 }
-                buf = h;
-                multiply_chunk<DT, GR, TM, TN>(w[h], frag, acc);
+            if (st + 1 < stages) {
+                if constexpr (n < S::NXR)
+                    s.template load_x<n>(st + 1);
+                else if constexpr (n - S::NXR < S::N)
+                    s.template load<n - S::NXR>(st + 1, late);
             }
-        }
-    } else {
-        Raw8<DT> x[NP];
-        auto load_x = [&](int c) {
-            if (c * 128 + 128 <= k) {
+            if constexpr (before >= 0 && before / TM % MG == MG - 1)
+                scale(before % TM, before / TM / MG);
+            if constexpr (m < 3)   // a share of the next weights
 #pragma unroll
-                for (int i = 0; i < NP; ++i)
-                    x[i] = ld_raw8<DT, false>(xbase + row_at(i), c * 128 + xu * 8, k);
-            } else {
+                for (int t = r * TN / TM; t < (r + 1) * TN / TM; ++t)
+                    b[(m + 1) & 1][t] = weights8(code[(m + 1) & 1][t]);
+            if constexpr (r == TM - 1 && m < 2)
 #pragma unroll
-                for (int i = 0; i < NP; ++i)
-                    x[i] = ld_raw8<DT, true>(xbase + row_at(i), c * 128 + xu * 8, k);
-            }
-        };
-        if (chunks > 0) {
-            load_x(0);
-            load_w(0, w[0]);
-        }
-        for (int c = 0; c < chunks; c += 2) {
+                for (int t = 0; t < TN; ++t)
+                    code[m & 1][t] = S::codes_of(now, row(t), m + 2, q);
+            if constexpr (r == 0 && m % MG == 0 && m + MG < 4)   // the scales before this group's have joined
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                if (c + h >= chunks)
-                    break;
-                __syncthreads();
-#pragma unroll
-                for (int i = 0; i < NP; ++i)
-                    store_x(0, i, x[i]);
-                __syncthreads();
-                if (c + h + 1 < chunks) {
-                    load_x(c + h + 1);
-                    load_w(c + h + 1, w[h ^ 1]);
-                }
-                multiply_chunk<DT, GR, TM, TN>(w[h], frag, acc);
-            }
-        }
+                for (int t = 0; t < TN; ++t)
+                    by[(m / MG + 1) & 1][t] = S::scale_of(now, row(t), m / MG + 1);
+            __builtin_amdgcn_sched_barrier(0);
+        });
+        scale(TM - 1, 3 / MG);
     }
 #pragma unroll
     for (int r = 0; r < TM; ++r)
 #pragma unroll
         for (int t = 0; t < TN; ++t)
-            put4<DT>(a, rows, rows.lo + (uint32_t)(wm + r * 16 + q * 4), n0 + (uint32_t)(wn + t * 16 + col), acc[r][t]);
+            put4<DT>(a, rows, rows.lo + (uint32_t)(wm + r * 16 + q * 4), n0 + (uint32_t)row(t), acc[r][t]);
 }
 
 // A call's workgroups: whole rounds of the XCDs for the tiles with an expert and
@@ -637,13 +745,6 @@ hipError_t launch_stream(GemmFp4Args& a, const char* name, hipStream_t s)
                        16 * NS, KS * NS * kWave, s);
 }
 
-template <int DT, int GR, int TM, int TN, int WM, int WN, bool DIRECT>
-hipError_t launch_tile(GemmFp4Args& a, hipStream_t s)
-{
-    return launch_grid(a, (const void*)k_gemm_fp4_tile<DT, GR, TM, TN, WM, WN, DIRECT>, "k_gemm_fp4_tile", 16 * TM * WM,
-                       16 * TN * WN, WM * WN * kWave, s);
-}
-
 // A kind of workgroup: its tile, how many a CU takes, and the microseconds that
 // 1024 of k take it alone on its CU, and with the CU full.
 struct Kind {
@@ -651,59 +752,67 @@ struct Kind {
 };
 
 // Estimated time. The kinds' figures are measured at 8192 and 4096 of k, with
-// groups of 128 (32: 5 to 15% more, alike for all). Up to one workgroup a CU runs at
-// `alone`; a CU that fills up goes over to `full`. With experts the number of tiles is known
-// to about half a tile each.
-inline double estimate(const GemmFp4Args& a, const Kind& x)
+// groups of 128 (32: 5 to 30% more, alike for all). CUs that are full, round by round, and
+// a last round that fills up from `alone` to `full`.
+inline double estimate(const GemmFp4Args& a, const Kind& x, double rows)
 {
     const double cus = device_cu_count();
-    double tm = (double)((a.rows + (size_t)x.bm - 1) / (size_t)x.bm);
-    if (a.offsets) {
-        const double owners = (double)a.experts < a.rows ? (double)a.experts : a.rows;
-        tm = a.rows / x.bm + 0.5 * owners;
+    double tm = (double)(long long)((rows + x.bm - 1.0) / x.bm);
+    if (a.offsets) {   // about half a tile of each expert is empty
+        const double owners = (double)a.experts < rows ? (double)a.experts : rows;
+        tm = rows / x.bm + 0.5 * owners;
         tm = tm < owners ? owners : tm;
     }
     const double tn = (double)((a.n + (size_t)x.bn - 1) / (size_t)x.bn), t = tm * tn / cus, k = a.k / 1024.0, start = 0.5;
     if (((double)row_tiles(a, (size_t)x.bm) * tn + 16.0) * 512.0 >= 4294967296.0)
         return 1e300;   // threads of one launch
-    if (t <= 1.0)
-        return start + k * x.alone;
-    if (t <= x.per_cu)
-        return start + k * (x.alone + (x.full - x.alone) * (t - 1.0) / (x.per_cu - 1.0));
-    const double r = t / x.per_cu, up = (double)(long long)r + (r > (double)(long long)r ? 1.0 : 0.0);
-    const double rounds = x.per_cu > 1.0 ? r + 0.25 < up ? r + 0.25 : up : a.offsets ? t + 0.5 : up;
-    return rounds * (start + k * x.full);
+    const double rounds = (double)(long long)(t / x.per_cu), rest = t - rounds * x.per_cu;
+    double time = rounds * (start + k * x.full);
+    if (rest > 0.0)
+        time += start + k * (rest > 1.0 ? x.alone + (x.full - x.alone) * (rest - 1.0) / (x.per_cu - 1.0) : x.alone);
+    return time;
+}
+
+// Rows that no expert has are only known on the device: as if all, and as if half had one.
+inline double estimate(const GemmFp4Args& a, const Kind& x)
+{
+    const double all = estimate(a, x, (double)a.rows);
+    return a.offsets ? 0.5 * (all + estimate(a, x, 0.5 * (double)a.rows)) : all;
 }
 
 // The kinds, and where another would go wrong (us, groups of 128):
-//   BF16                          16x16 16x32 16x64 32x32 32x128 64x32 64x128 128x128
+//   BF16                          16x16 16x32 16x64 32x32 32x128 64x32 64x128 128x256
 //   13 x 4096 x 8192                9.2  10.3
 //   16 x 8192 x 8192               15.0  11.4  38.9
 //   32 x 8192 x 8192                                 15.5  30.7
-//   64 x 8192 x 8192                                              22.4   52
-//   512 x 8192 x 8192                                              159   88    95
-//   1024 x 8192 x 8192                                                  182   161
+//   64 x 8192 x 8192                                              22.0   49
+//   128 x 8192 x 8192                                     34.9    42     50     99
+//   512 x 8192 x 8192                                              159   96     111
+//   1024 x 8192 x 8192                                                  179     124
 //   64 experts x 4 x 4096 x 4096          190   120
-//   64 experts x 24 x 4096 x 4096                     270   163
-//   64 experts x 48 x 4096 x 4096                                  415  240   340
-//   FP32                            few  16x32 16x64        32x128       64x128
+//   64 experts x 24 x 4096 x 4096                     270   162          231    269
+//   64 experts x 48 x 4096 x 4096                           254   415    252    276
+//   64 experts x 256 x 4096 x 4096                                       805    580
+//   FP32                            few  16x32 16x64        32x128       64x128 parts
 //   13 x 1000 x 2051                6.7   7.9
 //   16 x 8192 x 8192                 39    21
-//   512 x 8192 x 8192                                        246          214
+//   128 x 8192 x 8192                                         72          133
+//   512 x 8192 x 8192                                        228          190
 //   64 experts x 4 x 4096 x 4096          296   180
-//   64 experts x 48 x 4096 x 4096                            510          468
+//   12 experts x 129 x 2100 x 2056                            67           85
+//   64 experts x 48 x 4096 x 4096                            481          397
 template <int DT, int GR>
 hipError_t launch_fp4(const GemmFp4Args& in, hipStream_t s)
 {
     GemmFp4Args a = in;
     constexpr Kind kBf16[] = {{16, 32, 1, 1.05, 1.05}, {16, 64, 4, 2.6, 7.5}, {32, 32, 1, 1.6, 1.6}, {32, 128, 2, 3.5, 9.5},
-                              {64, 32, 1, 2.5, 2.5}, {64, 128, 2, 6.2, 10.6}, {128, 128, 2, 11.3, 19.7},
+                              {64, 32, 1, 2.5, 2.5}, {64, 128, 2, 6.2, 11.8}, {128, 256, 1, 13.8, 15.0},
                               {16, 16, 1, 0.75, 0.75}};
-    constexpr Kind kFp32[] = {{16, 32, 1, 2.2, 2.2}, {16, 64, 2, 4.3, 5.6}, {32, 128, 2, 8.1, 15.4}, {64, 128, 2, 20.0, 26.0},
+    constexpr Kind kFp32[] = {{16, 32, 1, 2.2, 2.2}, {16, 64, 2, 4.3, 5.6}, {32, 128, 2, 9.0, 15.1}, {64, 128, 2, 16.7, 23.8},
                               {16, 16, 1, 2.0, 2.0}};
     const bool whole = DT == 1 && (uintptr_t)a.a % 16 == 0 && a.ld_a % 8 == 0 && a.k % 8 == 0;
     const Kind* kinds = DT == 0 ? kFp32 : kBf16;
-    const int n = DT == 0 ? 5 : whole ? 8 : 7;
+    const int n = DT == 0 ? 5 : whole ? 8 : 6;   // rows by way of registers gain nothing from larger tiles
     int best = 0;
     double cost = 1e301;
     for (int i = 0; i < n; ++i) {
@@ -718,7 +827,7 @@ hipError_t launch_fp4(const GemmFp4Args& in, hipStream_t s)
         case 0: return launch_stream<0, GR, 1, 16, 4, 2, 512, 2, false>(a, "k_gemm_fp4_stream 16x32", s);
         case 1: return launch_stream<0, GR, 1, 16, 1, 4, 256, 2, false>(a, "k_gemm_fp4_stream 16x64", s);
         case 2: return launch_stream<0, GR, 2, 32, 1, 8, 128, 2, false>(a, "k_gemm_fp4_stream 32x128", s);
-        case 3: return launch_tile<0, GR, 4, 2, 1, 4, false>(a, s);
+        case 3: return launch_grid(a, (const void*)k_gemm_fp4_parts<GR>, "k_gemm_fp4_parts", 64, 128, 4 * kWave, s);
         default: return launch_grid(a, (const void*)k_gemm_fp4_few<0, GR>, "k_gemm_fp4_few", 16, 16, 8 * kWave, s);
         }
     } else if (whole) {
@@ -730,7 +839,7 @@ hipError_t launch_fp4(const GemmFp4Args& in, hipStream_t s)
         case 3: return launch_stream<1, GR, 2, 32, 1, 8, 256, 2, true>(a, "k_gemm_fp4_stream 32x128", s);
         case 4: return launch_stream<1, GR, 4, 64, 4, 2, 512, 2, true>(a, "k_gemm_fp4_stream 64x32", s);
         case 5: return launch_stream<1, GR, 4, 64, 1, 8, 128, 3, true>(a, "k_gemm_fp4_stream 64x128", s);
-        case 6: return launch_tile<1, GR, 4, 4, 2, 2, true>(a, s);
+        case 6: return launch_grid(a, (const void*)k_gemm_fp4_tile<GR>, "k_gemm_fp4_tile", 128, 256, 8 * kWave, s);
         default: return four ? launch_stream<1, GR, 1, 4, 8, 1, 1024, 2, true>(a, "k_gemm_fp4_stream 16x16, four rows", s) : launch_stream<1, GR, 1, 16, 8, 1, 1024, 2, true>(a, "k_gemm_fp4_stream 16x16", s);
         }
     } else {
@@ -740,8 +849,7 @@ hipError_t launch_fp4(const GemmFp4Args& in, hipStream_t s)
         case 2: return launch_stream<1, GR, 2, 32, 4, 2, 512, 3, false>(a, "k_gemm_fp4_stream 32x32, rows by way of registers", s);
         case 3: return launch_stream<1, GR, 2, 32, 1, 8, 256, 2, false>(a, "k_gemm_fp4_stream 32x128, rows by way of registers", s);
         case 4: return launch_stream<1, GR, 4, 64, 4, 2, 512, 2, false>(a, "k_gemm_fp4_stream 64x32, rows by way of registers", s);
-        case 5: return launch_stream<1, GR, 4, 64, 1, 8, 128, 3, false>(a, "k_gemm_fp4_stream 64x128, rows by way of registers", s);
-        default: return launch_tile<1, GR, 4, 4, 2, 2, false>(a, s);
+        default: return launch_stream<1, GR, 4, 64, 1, 8, 128, 3, false>(a, "k_gemm_fp4_stream 64x128, rows by way of registers", s);
         }
     }
 }

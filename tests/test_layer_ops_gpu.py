@@ -314,6 +314,31 @@ def test_gemm_fp4_rows_do_not_mix(m, n):
     assert bool(out[1].isnan().all()) and not bool(out[2].isfinite().all())
 
 
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("m,n,k,group", [(3, 40, 200, 64), (3, 20, 33, 32), (16, 5000, 520, 32), (200, 9000, 136, 32), (2000, 9000, 264, 64)])
+def test_gemm_fp4_infinite_scales(dtype, m, n, k, group):
+    """An infinite scale makes its channel infinite with its group's sign, also where a tile goes on behind k."""
+    g = gen(k)
+    full, code, scales = some_codes(g, n, k, group)
+    code[5, :group], full[5, :group // 2] = 2, 0x22     # ones
+    scales[5, 0] = torch.inf
+    a = randn(g, m, k, dtype=dtype).abs() + 1
+    out = torch.empty(m, n, dtype=dtype, device="cuda")
+    rx.rx_gemm_fp4(a.cuda(), full.cuda()[:, :(k + 1) // 2], scales.cuda(), out, group)
+    assert bool((out[:, 5] == torch.inf).all())
+    scales[5, 0] = 1.0
+    want, bound = R.gemm_fp4(a, code, scales, group)
+    rest = [i for i in range(n) if i != 5]
+    within(out[:, rest], want[:, rest], bound[:, rest])
+
+
+@pytest.mark.parametrize("group", [32, 64, 128])
+def test_gemm_fp4_grouped_many_rows(group):
+    """Large tiles that end inside an expert, an expert without rows and rows without an expert."""
+    test_gemm_fp4_grouped(BF16, [700, 0, 1300, 129], 300, 4100, 264, group)
+    test_gemm_fp4_grouped(torch.float32, [700, 0, 1300, 129], 300, 4100, 264, group)
+
+
 def test_gemm_fp4_without_columns_or_rows():
     b, s = torch.zeros(40, 0, dtype=torch.uint8, device="cuda"), torch.zeros(40, 0, **F32)
     out = torch.full((3, 40), 7.0, **F32)

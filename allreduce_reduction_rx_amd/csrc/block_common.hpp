@@ -49,14 +49,17 @@ __device__ __forceinline__ void st16_any_stream(void* p, u32x4 v)
 // A partial vector is the last whole one of the row, shifted: one load, where
 // one for every element would be a chain of up to seven. ld_raw loads and
 // fixed() shifts: between the two go the other loads, so that none waits.
-template <int DT, bool TAIL, bool NT = false>
+// Without SHORT a row is a vector long at least: the code for shorter ones
+// writes the same registers element by element, and a load in a loop would wait for
+// the one before it.
+template <int DT, bool TAIL, bool NT = false, bool SHORT = true>
 __device__ __forceinline__ u32x4 ld_raw(const void* row, int v, int hidden)
 {
     constexpr int VE = Elem<DT>::kVE;
     const int c = v * VE;
     const char* p = static_cast<const char*>(row);
     u32x4 x = {0, 0, 0, 0};
-    if (!TAIL || hidden >= VE) {
+    if (!TAIL || !SHORT || hidden >= VE) {
         const int at = !TAIL || c < hidden - VE ? c : hidden - VE;
         if (TAIL || c < hidden) {
             p += (uint32_t)at * (uint32_t)Elem<DT>::kBytes;

@@ -310,9 +310,9 @@ __global__ __launch_bounds__(WG, WG > 512 ? 4 : 2) void k_layer_norm_backward(La
 #pragma unroll
         for (int u = 0; u < NV; ++u) {
             const int v = tid + u * W;
-            hv[u] = a.d_z ? ld_raw<DT, TAIL, true>(static_cast<const char*>(a.h) + t * a.ld_h * EB, v, hidden) : zero;
-            dzv[u] = a.d_z ? ld_raw<DT, TAIL, true>(static_cast<const char*>(a.d_z) + t * a.ld_d_z * EB, v, hidden) : zero;
-            dhv[u] = a.d_h ? ld_raw<DT, TAIL, true>(static_cast<const char*>(a.d_h) + t * a.ld_d_h * EB, v, hidden) : zero;
+            hv[u] = a.d_z ? ld_raw<DT, TAIL, true, false>(static_cast<const char*>(a.h) + t * a.ld_h * EB, v, hidden) : zero;
+            dzv[u] = a.d_z ? ld_raw<DT, TAIL, true, false>(static_cast<const char*>(a.d_z) + t * a.ld_d_z * EB, v, hidden) : zero;
+            dhv[u] = a.d_h ? ld_raw<DT, TAIL, true, false>(static_cast<const char*>(a.d_h) + t * a.ld_d_h * EB, v, hidden) : zero;
         }
         if (a.d_z) {
             nmean = a.mean[t];
@@ -490,7 +490,9 @@ int narrow_lanes(size_t nvec)
 // How a gradient's rows are spread. Rows of up to 128 vectors take a wave's lanes or
 // fewer, in workgroups of 512 threads; longer ones two vectors a thread, and workgroups of 512 threads a
 // CU or one larger one: every part costs its sums' write and read. Rows beyond
-// what the registers hold (1024 vectors BF16, FP32 2048) go by columns in parts.
+// what the registers hold (1024 vectors BF16, FP32 2048) go by columns in parts, and
+// rows shorter than a vector, whose loads would take the others' speed (1111 x 5001
+// FP32 with dropout: 36 us with their code in the loop, 28 without).
 struct Spread {
     bool whole;                // k_layer_norm_backward
     unsigned threads, lanes;   // of a workgroup; of a row where it has several, else 0
@@ -501,7 +503,7 @@ Spread spread(size_t rows, size_t hidden, int dtype)
 {
     Spread s = {};
     const size_t nvec = vectors(hidden, dtype), cus = (size_t)device_cu_count();
-    s.whole = nvec <= (dtype ? 1024 : 2048);
+    s.whole = hidden >= (dtype ? 8 : 4) && nvec <= (dtype ? 1024 : 2048);
     size_t want;
     if (s.whole) {
         s.threads = threads_for((nvec + 1) / 2, 512);
@@ -544,7 +546,7 @@ const void* backward_fn(const Spread& s)
         return (const void*)k_layer_norm_backward<DT, TAIL, 2, 256, false, DROP>;
     if constexpr (DT == 0)
         if (s.nv > 2)
-            return (const void*)k_layer_norm_backward<DT, TAIL, 4, 512, false, DROP>;
+            return s.nv == 3 ? (const void*)k_layer_norm_backward<DT, TAIL, 3, 512, false, DROP> : (const void*)k_layer_norm_backward<DT, TAIL, 4, 512, false, DROP>;
     return (const void*)k_layer_norm_backward<DT, TAIL, 2, 512, false, DROP>;
 }
 template <int DT>

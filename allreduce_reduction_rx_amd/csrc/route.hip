@@ -16,14 +16,14 @@ namespace {
 // their values.
 template <int DT, int V> struct RawLogits { u32x4 v[V / Elem<DT>::kVE]; };
 
-template <int DT, int V>
+template <int DT, int G, int V>   // more than one lane: more than a vector of experts
 __device__ __forceinline__ RawLogits<DT, V> ld_logits(const void* row, int pos, int experts)
 {
     constexpr int N = V / Elem<DT>::kVE;
     RawLogits<DT, V> r;
 #pragma unroll
     for (int i = 0; i < N; ++i)
-        r.v[i] = ld_raw<DT, true>(row, pos * N + i, experts);
+        r.v[i] = ld_raw<DT, true, false, G == 1>(row, pos * N + i, experts);
     return r;
 }
 template <int DT, int V>
@@ -108,7 +108,7 @@ __global__ __launch_bounds__(kRouteWaves<V> * kWave) void k_route(RouteArgs a)
         const size_t t = t0 + sub;
         // an empty token's logits are loaded too: no wait for the mask
         const RawLogits<DT, V> raw =
-            ld_logits<DT, V>(static_cast<const char*>(a.logits) + (t < a.tokens ? t : a.tokens - 1) * a.ld * Elem<DT>::kBytes, pos, experts);
+            ld_logits<DT, G, V>(static_cast<const char*>(a.logits) + (t < a.tokens ? t : a.tokens - 1) * a.ld * Elem<DT>::kBytes, pos, experts);
         bool live = t < a.tokens && (!a.mask || a.mask[t]);
         float x[V];
         uint32_t key[V];
@@ -362,7 +362,7 @@ __global__ __launch_bounds__(256) void k_route_backward(RouteBwdArgs a)
     for (size_t t0 = ((size_t)blockIdx.x * kWaves + wave) * TW; t0 < a.tokens; t0 += step) {
         // all loads before anything waits
         const size_t t = t0 + sub, row = t < a.tokens ? t : a.tokens - 1;
-        const RawLogits<DT, V> raw = ld_logits<DT, V>(static_cast<const char*>(a.logits) + row * a.ld * Elem<DT>::kBytes, pos, experts);
+        const RawLogits<DT, V> raw = ld_logits<DT, G, V>(static_cast<const char*>(a.logits) + row * a.ld * Elem<DT>::kBytes, pos, experts);
         const float stored = a.lse[row], lse = t < a.tokens ? stored : -__builtin_inff();
         const size_t left = a.tokens - t0;
         const int n = (left < (size_t)TW ? (int)left : TW) * topk;
@@ -377,7 +377,7 @@ __global__ __launch_bounds__(256) void k_route_backward(RouteBwdArgs a)
             u32x4 c[V / 4];
 #pragma unroll
             for (int i = 0; i < V / 4; ++i)
-                c[i] = ld_raw<0, true>(a.counts, pos * (V / 4) + i, experts);
+                c[i] = ld_raw<0, true, false, G == 1>(a.counts, pos * (V / 4) + i, experts);
             const int tokens = a.counts[experts];
             const float d0 = a.d_losses[0], d1 = a.d_losses[1], inv = tokens > 0 ? 1.0f / (float)tokens : 0.0f;
             const float by = d0 * ((float)experts / (float)topk) * inv * inv;

@@ -342,7 +342,8 @@ __device__ __forceinline__ void open_stage(bool next)
 
 // Few rows: 16 TT rows x 16 NS channels a workgroup of KS x NS waves, KC of k a
 // stage, NBUF - 1 stages on their way. A wave has 16 channels and every KS-th part of a
-// stage; the KS sums meet in LDS in their order.
+// stage; the KS sums meet in LDS in their order. Bound by the weights' bytes, and by
+// the rows that every workgroup reads again (1 x 8192 x 8192: 9.4 us for 36 MB; 32 rows: 16).
 template <int DT, int GR, int TT, int TR, int KS, int NS, int KC, int NBUF, bool WHOLE>
 __global__ __launch_bounds__(KS * NS * kWave) void k_gemm_fp4_stream(GemmFp4Args a)
 {
@@ -512,7 +513,9 @@ __device__ __forceinline__ void keep(f32x4 (&x)[N])
 // the next is read, the next 32's weights are made (their values are exact in BF16),
 // the scales join the sums of the step before, and a later stage asks for its share:
 // all loads at once would hold the wave up for as long as the cache takes them. A stage
-// is opened before the one before has ended, so that its first steps find their operands.
+// is opened before the one before has ended, so that its first steps find their
+// operands. 1024 x 8192 x 8192: 118 to 129 us (1.07 to 1.17 PFLOP/s), 140 with stages one after
+// the other, 160 in 128 x 128 tiles whose waves loaded their weights themselves.
 template <int GR>
 __global__ __launch_bounds__(8 * kWave, 2) void k_gemm_fp4_tile(GemmFp4Args a)
 {

@@ -612,9 +612,11 @@ rx_status_t rx_quant_fp4(const void* x, size_t ld_x, size_t rows, size_t k,
  *   out[m, j] = cast( sum over groups g of b_scales[j, g]
  *                     sum over i in g of a[m, i] b[j, i] )
  * The products are exact and the sums in FP32 (a in FP32 is taken apart into
- * three BF16 parts without loss, but for bits below 2^-133). offsets and experts
- * as in rx_gemm_i8: b's matrix e starts at b + e stride_b, its scales at
- * b_scales + e n ceil(k / group), and the rows past offsets[experts] become 0.
+ * three BF16 parts without loss, but for bits below 2^-133). A NaN or an infinity
+ * of a stays in its row: NaN, or with BF16 what the sums make of the infinity.
+ * offsets and experts as in rx_gemm_i8: b's matrix e starts at b + e stride_b, its
+ * scales at b_scales + e n ceil(k / group), and the rows past offsets[experts]
+ * become 0.
  *
  * a, out  : dtype (RX_FP32 or RX_BF16).
  * b       : 16-byte aligned; ld_b (bytes) and stride_b multiples of 16, ld_b at

@@ -521,7 +521,7 @@ Spread spread(size_t rows, size_t hidden, int dtype)
         if (rows <= 2 * teams)
             want = 1;
     } else {
-        const size_t blocks = (nvec + kWave - 1) / kWave;   // about four workgroups a CU over all columns
+        const size_t blocks = nvec ? (nvec + kWave - 1) / kWave : 1;   // about four workgroups a CU over all columns
         want = (4 * cus + blocks - 1) / blocks;
         if (want > (rows + 3) / 4)
             want = (rows + 3) / 4;

@@ -609,6 +609,21 @@ def test_layer_row_offsets_past_32_bits():
     within(o[1:], *R.gemm_fp4(a[1:], parts[1][1], parts[1][2], 32))
 
 
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("m,n,k", [(2000, 9000, 264), (13, 40, 200)])
+def test_gemm_fp4_with_the_widest_row_stride(dtype, m, n, k):
+    """Rows as far apart as they may be: 34 and 67 GB of them, tiles whose own rows span 2^31 bytes."""
+    g = gen(12)
+    full, code, scales = some_codes(g, n, k, 64)
+    a = randn(g, m, k, dtype=dtype)
+    ld = (1 << 23) - 8
+    far = torch.as_strided(torch.empty((m - 1) * ld + k, dtype=dtype, device="cuda"), (m, k), (ld, 1))
+    far.copy_(a)
+    out = torch.empty(m, n, dtype=dtype, device="cuda")
+    rx.rx_gemm_fp4(far, full.cuda()[:, :(k + 1) // 2], scales.cuda(), out, 64)
+    within(out, *R.gemm_fp4(a, code, scales, 64))
+
+
 class Block:
     """Buffers of one pass: route, dispatch, 4-bit products, combine, the block's end, and the gradients."""
 

@@ -197,8 +197,9 @@ struct Stager {
     static_assert(kX % kWave == 0 && kW % kWave == 0 && kS / SU % kWave == 0, "");
     static_assert((kX % T == 0 || kX < T) && (kW % T == 0 || kW < T) && (kS / SU % T == 0 || kS / SU < T), "");
     static_assert(WHOLE || ((UX >= kWave ? UX % kWave == 0 : kWave % UX == 0) && (BM * UX % T == 0 || BM * UX < T)), "");
+    static constexpr int RX = TR < 16 ? TR : BM;   // fewer than a fragment's: its other rows are these again
     struct Rows {
-        u32x4 x[P][BM * UX];
+        u32x4 x[P][RX * UX];
     };
     struct Weights {
         u32x4 w[kW];
@@ -312,6 +313,7 @@ struct Stager {
     static __device__ __forceinline__ Parts8<DT> rows_of(const Rows& st, int r, int k0)
     {
         Parts8<DT> f;
+        r = TR < 16 ? r % TR : r;
 #pragma unroll
         for (int p = 0; p < P; ++p)
             f.p[p] = __builtin_bit_cast(bf16x8, st.x[p][r * UX + (k0 / 8 ^ (r & 15))]);
@@ -341,17 +343,34 @@ __device__ __forceinline__ void open_stage(bool next)
 }
 
 // Few rows: 16 TT rows x 16 NS channels a workgroup of KS x NS waves, KC of k a
-// stage, NBUF - 1 stages on their way. A wave has 16 channels and every KS-th part of a
+// stage, DX - 1 stages of rows and DW - 1 of weights on their way. How many pays is
+// measured: 64 x 8192 x 8192 with weights from memory 34.5 us with one of each and 27.5
+// with two of weights, 13 x 4096 x 8192 12.0 with one of each, 9.1 with two and three, but
+// 256 rows of 64 experts, whose three or four workgroups a CU wait for each other less, 17.8
+// with one and 21 with two. A wave has 16 channels and every KS-th part of a
 // stage; the KS sums meet in LDS in their order. Bound by the weights' bytes, and by
 // the rows that every workgroup reads again (1 x 8192 x 8192: 9.4 us for 36 MB; 32 rows: 16).
-template <int DT, int GR, int TT, int TR, int KS, int NS, int KC, int NBUF, bool WHOLE>
+template <int DT, int GR, int TT, int TR, int KS, int NS, int KC, int DX, int DW, bool WHOLE>
 __global__ __launch_bounds__(KS * NS * kWave) void k_gemm_fp4_stream(GemmFp4Args a)
 {
     constexpr int BM = 16 * TT, BN = 16 * NS, SG = 128 / GR, KW = KC / KS;
     using S = Stager<DT, GR, BM, BN, TR, KC, KS * NS * kWave, WHOLE>;
-    static_assert(KW % 128 == 0 && (NBUF == 2 || NBUF == 3), "");
-    __shared__ __align__(16) typename S::Stage ring[NBUF];
-    static_assert(sizeof(ring) >= sizeof(f32x4) * KS * NS * TT * kWave && sizeof(ring) <= 160 * 1024, "");
+    constexpr int NWS = S::N - S::NX;
+    static_assert(KW % 128 == 0 && DX >= 2 && DW >= DX && (WHOLE || DX == DW), "");
+    // as many of both: one ring, whose places take one offset (one ring 114 us for 32 x 8
+    // rows of 64 experts, two 119)
+    constexpr bool ONE = DX == DW;
+    __shared__ __align__(16) typename S::Stage ring[DX];
+    __shared__ __align__(16) typename S::Rows xring[DX];
+    __shared__ __align__(16) typename S::Weights wring[DW];
+    static_assert((ONE ? sizeof(ring) : sizeof(xring) + sizeof(wring)) <= 160 * 1024, "");
+    static_assert(KS == 1 || sizeof(xring) >= sizeof(f32x4) * KS * NS * TT * kWave, "");
+    auto rows_at = [&](int b) -> typename S::Rows& {
+        if constexpr (ONE) return ring[b]; else return xring[b];
+    };
+    auto weights_at = [&](int b) -> typename S::Weights& {
+        if constexpr (ONE) return ring[b]; else return wring[b];
+    };
     const int lane = lane_id(), wave = wave_id(), ks = wave % KS, ns = wave / KS, col = lane % 16, q = lane / 16;
     const Tiles tiles = count_tiles(a, BM);
     uint32_t tm, tn;
@@ -369,7 +388,7 @@ __global__ __launch_bounds__(KS * NS * kWave) void k_gemm_fp4_stream(GemmFp4Args
     const int k = (int)a.k, stages = (k + KC - 1) / KC;
     f32x4 acc[TT] = {};
     // this wave's part of a stage
-    auto multiply = [&](const typename S::Stage& st, int left) {
+    auto multiply = [&](const typename S::Rows& xs, const typename S::Weights& ws, int left) {
 #pragma unroll
         for (int j = 0; j < KW / 128; ++j) {
             const int k0 = ks * KW + j * 128;
@@ -377,34 +396,52 @@ __global__ __launch_bounds__(KS * NS * kWave) void k_gemm_fp4_stream(GemmFp4Args
                 break;
             const int r = ns * 16 + col;
             Coded<GR> w;
-            w.codes = st.w[r * S::UW + S::wplace(r, k0 / 32 + q)];
+            w.codes = ws.w[r * S::UW + S::wplace(r, k0 / 32 + q)];
 #pragma unroll
             for (int g = 0; g < SG; ++g)
-                w.scale[g] = S::scale_of(st, r, k0 / GR + g);
-            multiply_chunk<DT, GR, TT>(w, [&](int t, int m) { return S::rows_of(st, t * 16 + col, k0 + m * 32 + q * 8); }, acc);
+                w.scale[g] = S::scale_of(ws, r, k0 / GR + g);
+            multiply_chunk<DT, GR, TT>(w, [&](int t, int m) { return S::rows_of(xs, t * 16 + col, k0 + m * 32 + q * 8); }, acc);
         }
     };
     auto load_x = [&](int st) {
         unrolled<S::NXR>([&](auto i) { s.template load_x<i()>(st); });
         order();
     };
-    auto load = [&](int st, int buf) { unrolled<S::N>([&](auto i) { s.template load<i()>(st, ring[buf]); }); };
+    auto load_rows = [&](int st, typename S::Rows& to) { unrolled<S::NX>([&](auto i) { s.template load<i()>(st, to); }); };
+    auto load_weights = [&](int st, typename S::Weights& to) { unrolled<NWS>([&](auto i) { s.template load<S::NX + i()>(st, to); }); };
     if (S::NXR > 0 && stages > 0)
         load_x(0);
 #pragma unroll
-    for (int st = 0; st < NBUF - 1; ++st)
-        if (st < stages)
-            load(st, st);
-    int buf = 0;
+    for (int at = 1 - DW; at < 0; ++at) {   // as if the stages before had sent them
+        if (at + DX > 0 && at + DX - 1 < stages)
+            load_rows(at + DX - 1, rows_at((at + DX - 1) % DX));
+        if (at + DW > 0 && at + DW - 1 < stages)
+            load_weights(at + DW - 1, weights_at((at + DW - 1) % DW));
+    }
+    int bx = 0, bw = 0;
     for (int st = 0; st < stages; ++st) {
-        s.store_x(ring[buf]);
-        open_stage<(NBUF - 2) * S::N>(st + 1 < stages);
+        s.store_x(rows_at(bx));
+        // Loads return in their order: what went out after this stage's rows (which,
+        // with DW > DX, went out after its weights) may still be on its way.
+        if (ONE)
+            open_stage<(DX - 2) * S::N>(st + DX - 2 < stages);
+        else if (st + DW - 2 < stages)
+            open_stage<(DX - 2) * S::N + NWS>(true);
+        else
+            open_stage<(DX - 2) * S::NX>(st + DX - 2 < stages);
         if (S::NXR > 0 && st + 1 < stages)
             load_x(st + 1);
-        if (st + NBUF - 1 < stages)
-            load(st + NBUF - 1, buf == 0 ? NBUF - 1 : buf - 1);
-        multiply(ring[buf], k - st * KC);
-        buf = buf + 1 == NBUF ? 0 : buf + 1;
+        const int nx = bx == 0 ? DX - 1 : bx - 1, nw = bw == 0 ? DW - 1 : bw - 1;   // the places that were read last
+        if (st + DX - 1 < stages) {
+            load_rows(st + DX - 1, rows_at(nx));
+            if (ONE)
+                load_weights(st + DW - 1, weights_at(nx));
+        }
+        if (!ONE && st + DW - 1 < stages)
+            load_weights(st + DW - 1, weights_at(nw));
+        multiply(rows_at(bx), weights_at(ONE ? bx : bw), k - st * KC);
+        bx = bx + 1 == DX ? 0 : bx + 1;
+        bw = bw + 1 == DW ? 0 : bw + 1;
     }
     auto put = [&](int t, int group, f32x4 v) {
         put4<DT>(a, rows, rows.lo + (uint32_t)(t * 16 + q * 4), n0 + (uint32_t)(group * 16 + col), v);
@@ -414,7 +451,7 @@ __global__ __launch_bounds__(KS * NS * kWave) void k_gemm_fp4_stream(GemmFp4Args
         for (int t = 0; t < TT; ++t)
             put(t, ns, acc[t]);
     } else {
-        f32x4* joined = reinterpret_cast<f32x4*>(&ring[0]);
+        f32x4* joined = reinterpret_cast<f32x4*>(&rows_at(0));
         __syncthreads();
 #pragma unroll
         for (int t = 0; t < TT; ++t)
@@ -741,10 +778,10 @@ inline hipError_t launch_grid(GemmFp4Args& a, const void* fn, const char* name, 
     return launch_logged(name, fn, dim3((unsigned)grid), dim3(threads), params, s);
 }
 
-template <int DT, int GR, int TT, int TR, int KS, int NS, int KC, int NBUF, bool WHOLE>
+template <int DT, int GR, int TT, int TR, int KS, int NS, int KC, int DX, int DW, bool WHOLE>
 hipError_t launch_stream(GemmFp4Args& a, const char* name, hipStream_t s)
 {
-    return launch_grid(a, (const void*)k_gemm_fp4_stream<DT, GR, TT, TR, KS, NS, KC, NBUF, WHOLE>, name, 16 * TT,
+    return launch_grid(a, (const void*)k_gemm_fp4_stream<DT, GR, TT, TR, KS, NS, KC, DX, DW, WHOLE>, name, 16 * TT,
                        16 * NS, KS * NS * kWave, s);
 }
 
@@ -785,10 +822,11 @@ inline double estimate(const GemmFp4Args& a, const Kind& x)
 
 // The kinds, and where another would go wrong (us, groups of 128):
 //   BF16                          16x16 16x32 16x64 32x32 32x128 64x32 64x128 128x256
-//   13 x 4096 x 8192                9.2  10.3
-//   16 x 8192 x 8192               15.0  11.4  38.9
+//   13 x 4096 x 8192                8.6  10.4
+//   16 x 8192 x 8192               15.5  11.8  38.9
 //   32 x 8192 x 8192                                 15.5  30.7
-//   64 x 8192 x 8192                                              22.0   49
+//   64 x 8192 x 8192                                              24.5   49
+//   64 x 4096 x 4096                            9.5               12.5
 //   128 x 8192 x 8192                                     34.9    42     50     99
 //   512 x 8192 x 8192                                              159   96     111
 //   1024 x 8192 x 8192                                                  179     124
@@ -809,8 +847,8 @@ hipError_t launch_fp4(const GemmFp4Args& in, hipStream_t s)
 {
     GemmFp4Args a = in;
     constexpr Kind kBf16[] = {{16, 32, 1, 1.05, 1.05}, {16, 64, 4, 2.6, 7.5}, {32, 32, 1, 1.6, 1.6}, {32, 128, 2, 3.5, 9.5},
-                              {64, 32, 1, 2.5, 2.5}, {64, 128, 2, 6.2, 11.8}, {128, 256, 1, 13.8, 15.0},
-                              {16, 16, 1, 0.75, 0.75}};
+                              {64, 32, 1, 2.3, 2.3}, {64, 128, 2, 6.2, 11.8}, {128, 256, 1, 13.8, 15.0},
+                              {16, 16, 1, 0.6, 0.6}};
     constexpr Kind kFp32[] = {{16, 32, 1, 2.2, 2.2}, {16, 64, 2, 4.3, 5.6}, {32, 128, 2, 9.0, 15.1}, {64, 128, 2, 16.7, 23.8},
                               {16, 16, 1, 2.0, 2.0}};
     const bool whole = DT == 1 && (uintptr_t)a.a % 16 == 0 && a.ld_a % 8 == 0 && a.k % 8 == 0;
@@ -827,32 +865,32 @@ hipError_t launch_fp4(const GemmFp4Args& in, hipStream_t s)
     }
     if constexpr (DT == 0) {
         switch (best) {
-        case 0: return launch_stream<0, GR, 1, 16, 4, 2, 512, 2, false>(a, "k_gemm_fp4_stream 16x32", s);
-        case 1: return launch_stream<0, GR, 1, 16, 1, 4, 256, 2, false>(a, "k_gemm_fp4_stream 16x64", s);
-        case 2: return launch_stream<0, GR, 2, 32, 1, 8, 128, 2, false>(a, "k_gemm_fp4_stream 32x128", s);
+        case 0: return launch_stream<0, GR, 1, 16, 4, 2, 512, 2, 2, false>(a, "k_gemm_fp4_stream 16x32", s);
+        case 1: return launch_stream<0, GR, 1, 16, 1, 4, 256, 2, 2, false>(a, "k_gemm_fp4_stream 16x64", s);
+        case 2: return launch_stream<0, GR, 2, 32, 1, 8, 128, 2, 2, false>(a, "k_gemm_fp4_stream 32x128", s);
         case 3: return launch_grid(a, (const void*)k_gemm_fp4_parts<GR>, "k_gemm_fp4_parts", 64, 128, 4 * kWave, s);
         default: return launch_grid(a, (const void*)k_gemm_fp4_few<0, GR>, "k_gemm_fp4_few", 16, 16, 8 * kWave, s);
         }
     } else if (whole) {
         const bool four = a.rows <= 4;   // fewer rows to load: 1 x 8192 x 8192 9.9 against 11.2 us
         switch (best) {
-        case 0: return four ? launch_stream<1, GR, 1, 4, 4, 2, 1024, 3, true>(a, "k_gemm_fp4_stream 16x32, four rows", s) : launch_stream<1, GR, 1, 16, 4, 2, 1024, 3, true>(a, "k_gemm_fp4_stream 16x32", s);
-        case 1: return launch_stream<1, GR, 1, 16, 1, 4, 256, 2, true>(a, "k_gemm_fp4_stream 16x64", s);
-        case 2: return launch_stream<1, GR, 2, 32, 4, 2, 512, 3, true>(a, "k_gemm_fp4_stream 32x32", s);
-        case 3: return launch_stream<1, GR, 2, 32, 1, 8, 256, 2, true>(a, "k_gemm_fp4_stream 32x128", s);
-        case 4: return launch_stream<1, GR, 4, 64, 4, 2, 512, 2, true>(a, "k_gemm_fp4_stream 64x32", s);
-        case 5: return launch_stream<1, GR, 4, 64, 1, 8, 128, 3, true>(a, "k_gemm_fp4_stream 64x128", s);
+        case 0: return four ? launch_stream<1, GR, 1, 4, 4, 2, 1024, 3, 3, true>(a, "k_gemm_fp4_stream 16x32, four rows", s) : launch_stream<1, GR, 1, 16, 4, 2, 1024, 3, 3, true>(a, "k_gemm_fp4_stream 16x32", s);
+        case 1: return launch_stream<1, GR, 1, 16, 1, 4, 256, 2, 2, true>(a, "k_gemm_fp4_stream 16x64", s);
+        case 2: return launch_stream<1, GR, 2, 32, 4, 2, 512, 3, 3, true>(a, "k_gemm_fp4_stream 32x32", s);
+        case 3: return launch_stream<1, GR, 2, 32, 1, 8, 256, 2, 2, true>(a, "k_gemm_fp4_stream 32x128", s);
+        case 4: return launch_stream<1, GR, 4, 64, 4, 2, 512, 2, 3, true>(a, "k_gemm_fp4_stream 64x32", s);
+        case 5: return launch_stream<1, GR, 4, 64, 1, 8, 128, 3, 3, true>(a, "k_gemm_fp4_stream 64x128", s);
         case 6: return launch_grid(a, (const void*)k_gemm_fp4_tile<GR>, "k_gemm_fp4_tile", 128, 256, 8 * kWave, s);
-        default: return four ? launch_stream<1, GR, 1, 4, 8, 1, 1024, 2, true>(a, "k_gemm_fp4_stream 16x16, four rows", s) : launch_stream<1, GR, 1, 16, 8, 1, 1024, 2, true>(a, "k_gemm_fp4_stream 16x16", s);
+        default: return four ? launch_stream<1, GR, 1, 4, 8, 1, 1024, 4, 4, true>(a, "k_gemm_fp4_stream 16x16, four rows", s) : launch_stream<1, GR, 1, 16, 8, 1, 1024, 3, 4, true>(a, "k_gemm_fp4_stream 16x16", s);
         }
     } else {
         switch (best) {
-        case 0: return launch_stream<1, GR, 1, 16, 4, 2, 1024, 3, false>(a, "k_gemm_fp4_stream 16x32, rows by way of registers", s);
-        case 1: return launch_stream<1, GR, 1, 16, 1, 4, 256, 2, false>(a, "k_gemm_fp4_stream 16x64, rows by way of registers", s);
-        case 2: return launch_stream<1, GR, 2, 32, 4, 2, 512, 3, false>(a, "k_gemm_fp4_stream 32x32, rows by way of registers", s);
-        case 3: return launch_stream<1, GR, 2, 32, 1, 8, 256, 2, false>(a, "k_gemm_fp4_stream 32x128, rows by way of registers", s);
-        case 4: return launch_stream<1, GR, 4, 64, 4, 2, 512, 2, false>(a, "k_gemm_fp4_stream 64x32, rows by way of registers", s);
-        default: return launch_stream<1, GR, 4, 64, 1, 8, 128, 3, false>(a, "k_gemm_fp4_stream 64x128, rows by way of registers", s);
+        case 0: return launch_stream<1, GR, 1, 16, 4, 2, 1024, 3, 3, false>(a, "k_gemm_fp4_stream 16x32, rows by way of registers", s);
+        case 1: return launch_stream<1, GR, 1, 16, 1, 4, 256, 2, 2, false>(a, "k_gemm_fp4_stream 16x64, rows by way of registers", s);
+        case 2: return launch_stream<1, GR, 2, 32, 4, 2, 512, 3, 3, false>(a, "k_gemm_fp4_stream 32x32, rows by way of registers", s);
+        case 3: return launch_stream<1, GR, 2, 32, 1, 8, 256, 2, 2, false>(a, "k_gemm_fp4_stream 32x128, rows by way of registers", s);
+        case 4: return launch_stream<1, GR, 4, 64, 4, 2, 512, 2, 2, false>(a, "k_gemm_fp4_stream 64x32, rows by way of registers", s);
+        default: return launch_stream<1, GR, 4, 64, 1, 8, 128, 3, 3, false>(a, "k_gemm_fp4_stream 64x128, rows by way of registers", s);
         }
     }
 }

@@ -280,12 +280,14 @@ __global__ __launch_bounds__(256) void k_layer_norm_columns(LayerNormBwdArgs a)
 // A row's vectors in registers, its two sums across the threads that hold it, and
 // the parameters' sums of a range of rows (a part) in registers too: every input is
 // read once. Several teams of a.lanes lanes (a power of two up to a wave) have a row
-// each where TEAMS; the next row's loads go out
-// as soon as this row's are unpacked, before its sums and stores. 16384 x 8192 BF16
-// with dropout and all outputs: 250 us for 1.34 GB (5.4 TB/s), 340 by k_layer_norm_means and
-// k_layer_norm_columns, which read h and d_z twice.
+// each where TEAMS; the next row's loads go out as soon as this row's are
+// unpacked, before its sums and stores, and the next two rows' where a workgroup has a CU
+// for itself (16384 x 8192 BF16 with dropout, forward and gradient 474 us, 486 with one; 8192 x 4096,
+// two workgroups a CU, 89 and 87). 16384 x 8192 BF16 with dropout and all outputs: 245 us for
+// 1.34 GB (5.5 TB/s), 340 by k_layer_norm_means and k_layer_norm_columns, which read h and
+// d_z twice.
 template <int DT, bool TAIL, int NV, int WG, bool TEAMS, bool DROP>
-__global__ __launch_bounds__(WG, WG > 512 ? 4 : 2) void k_layer_norm_backward(LayerNormBwdArgs a)
+__global__ __launch_bounds__(WG, 2) void k_layer_norm_backward(LayerNormBwdArgs a)
 {
     constexpr int VE = Elem<DT>::kVE, EB = Elem<DT>::kBytes, E = NV * VE;
     __shared__ float sums[2 * 16 * 2];
@@ -300,38 +302,37 @@ __global__ __launch_bounds__(WG, WG > 512 ? 4 : 2) void k_layer_norm_backward(La
     Dropper d = {};
     if (DROP)
         d = dropper(a);
-    u32x4 w[NV], hv[NV], dhv[NV], dzv[NV];
+    constexpr int D = NV == 2 && WG == 512 && !TEAMS ? 2 : 1;   // rows ahead
+    struct Row {
+        u32x4 h[NV], dh[NV], dz[NV];
+        float mean, rstd;
+    } ahead[D];
+    u32x4 w[NV];
     float acc_w[E] = {}, acc_b[E] = {}, acc_bias[E] = {};
 #pragma unroll
     for (int u = 0; u < NV; ++u)
         w[u] = a.w ? ld_row<DT, TAIL>(a.w, tid + u * W, hidden) : u32x4{one, one, one, one};
-    float nmean = 0.0f, nrstd = 0.0f;
-    auto load = [&](size_t t) {
+    auto load = [&](Row& to, size_t t) {
 #pragma unroll
         for (int u = 0; u < NV; ++u) {
             const int v = tid + u * W;
-            hv[u] = a.d_z ? ld_raw<DT, TAIL, true, false>(static_cast<const char*>(a.h) + t * a.ld_h * EB, v, hidden) : zero;
-            dzv[u] = a.d_z ? ld_raw<DT, TAIL, true, false>(static_cast<const char*>(a.d_z) + t * a.ld_d_z * EB, v, hidden) : zero;
-            dhv[u] = a.d_h ? ld_raw<DT, TAIL, true, false>(static_cast<const char*>(a.d_h) + t * a.ld_d_h * EB, v, hidden) : zero;
+            to.h[u] = a.d_z ? ld_raw<DT, TAIL, true, false>(static_cast<const char*>(a.h) + t * a.ld_h * EB, v, hidden) : zero;
+            to.dz[u] = a.d_z ? ld_raw<DT, TAIL, true, false>(static_cast<const char*>(a.d_z) + t * a.ld_d_z * EB, v, hidden) : zero;
+            to.dh[u] = a.d_h ? ld_raw<DT, TAIL, true, false>(static_cast<const char*>(a.d_h) + t * a.ld_d_h * EB, v, hidden) : zero;
         }
-        if (a.d_z) {
-            nmean = a.mean[t];
-            nrstd = a.rstd[t];
-        }
+        to.mean = a.d_z ? a.mean[t] : 0.0f;
+        to.rstd = a.d_z ? a.rstd[t] : 0.0f;
     };
-    size_t t = r0 + team;
-    if (t < r1)
-        load(t);
-    for (; t < r1; t += R) {
-        const float mean = nmean, rstd = nrstd;
+    auto step = [&](Row& now, size_t t) {
+        const float mean = now.mean, rstd = now.rstd;
         float x[NV][VE], g[NV][VE], o[NV][VE], s[2] = {0.0f, 0.0f};
 #pragma unroll
         for (int u = 0; u < NV; ++u) {
             float wf[VE];
             auto whole = [&](u32x4 y) { return fixed<DT, TAIL>(y, tid + u * W, hidden); };
-            unpack<DT>(whole(hv[u]), x[u]);
-            unpack<DT>(whole(dzv[u]), g[u]);
-            unpack<DT>(whole(dhv[u]), o[u]);
+            unpack<DT>(whole(now.h[u]), x[u]);
+            unpack<DT>(whole(now.dz[u]), g[u]);
+            unpack<DT>(whole(now.dh[u]), o[u]);
             unpack<DT>(w[u], wf);
 #pragma unroll
             for (int k = 0; k < VE; ++k) {
@@ -343,8 +344,8 @@ __global__ __launch_bounds__(WG, WG > 512 ? 4 : 2) void k_layer_norm_backward(La
                 s[1] = __builtin_fmaf(g[u][k], x[u][k], s[1]);
             }
         }
-        if (t + R < r1)
-            load(t + R);
+        if (t + D * R < r1)
+            load(now, t + D * R);
         if constexpr (TEAMS) {
             s[0] = group_sum_rt(s[0], W);
             s[1] = group_sum_rt(s[1], W);
@@ -370,7 +371,16 @@ __global__ __launch_bounds__(WG, WG > 512 ? 4 : 2) void k_layer_norm_backward(La
             if (a.d_src)
                 st_row<DT, TAIL, true>(static_cast<char*>(a.d_src) + t * a.ld_d_src * EB, v, hidden, pack<DT>(o[u]));
         }
-    }
+    };
+#pragma unroll
+    for (int d = 0; d < D; ++d)
+        if (r0 + team + d * R < r1)
+            load(ahead[d], r0 + team + d * R);
+    for (size_t t = r0 + team; t < r1; t += D * R)
+#pragma unroll
+        for (int d = 0; d < D; ++d)
+            if (t + d * R < r1)
+                step(ahead[d], t + d * R);
     if (!a.d_w && !a.d_b && !a.d_bias)
         return;
 #pragma unroll

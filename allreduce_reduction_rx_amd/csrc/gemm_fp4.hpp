@@ -349,7 +349,7 @@ __device__ __forceinline__ void open_stage(bool next)
 // 256 rows of 64 experts, whose three or four workgroups a CU wait for each other less, 17.8
 // with one and 21 with two. A wave has 16 channels and every KS-th part of a
 // stage; the KS sums meet in LDS in their order. Bound by the weights' bytes, and by
-// the rows that every workgroup reads again (1 x 8192 x 8192: 9.4 us for 36 MB; 32 rows: 16).
+// the rows that every workgroup reads again (1 x 8192 x 8192: 9.2 us for 36 MB; 32 rows: 16).
 template <int DT, int GR, int TT, int TR, int KS, int NS, int KC, int DX, int DW, bool WHOLE>
 __global__ __launch_bounds__(KS * NS * kWave) void k_gemm_fp4_stream(GemmFp4Args a)
 {

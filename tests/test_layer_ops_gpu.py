@@ -274,6 +274,17 @@ def test_gemm_fp4_tiles(dtype, group, m, n, k, odd):
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("m,n,ks", [
+    (3, 600, (900, 1024, 2048, 2056, 3100, 4100, 5128, 6200)), (13, 600, (900, 1024, 2048, 2056, 3100, 4100, 5128, 6200)),
+    (16, 6000, (1000, 2048, 3100, 4104)), (30, 5000, (512, 520, 1100, 1600, 2100)), (60, 5000, (300, 512, 520, 1100, 1600, 2100)),
+    (200, 6000, (8, 128, 136, 392, 520)), (2000, 9000, (8, 64, 128, 256, 640))])
+def test_gemm_fp4_of_every_number_of_stages(dtype, m, n, ks):
+    """k from one stage of a tile's buffers to more than there are of them, whole and partial."""
+    for i, k in enumerate(ks):
+        check_gemm(dtype, m, n, k, (32, 64, 128)[i % 3])
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
 @pytest.mark.parametrize("counts,pad,n,k,group", [
     ([1], 0, 5, 40, 32), ([0, 3, 0, 1], 2, 20, 100, 64), ([4] * 16, 0, 40, 260, 128), ([20, 0, 33, 1, 70], 9, 130, 514, 32),
     ([0, 0], 4, 33, 64, 64), ([300, 5, 0, 129], 17, 70, 300, 64), ([1] * 70, 3, 33, 200, 128), ([2, 500], 1, 300, 129, 128)])

@@ -287,7 +287,8 @@ def test_gemm_fp4_of_every_number_of_stages(dtype, m, n, ks):
 @pytest.mark.parametrize("dtype", DTYPES)
 @pytest.mark.parametrize("counts,pad,n,k,group", [
     ([1], 0, 5, 40, 32), ([0, 3, 0, 1], 2, 20, 100, 64), ([4] * 16, 0, 40, 260, 128), ([20, 0, 33, 1, 70], 9, 130, 514, 32),
-    ([0, 0], 4, 33, 64, 64), ([300, 5, 0, 129], 17, 70, 300, 64), ([1] * 70, 3, 33, 200, 128), ([2, 500], 1, 300, 129, 128)])
+    ([0, 0], 4, 33, 64, 64), ([300, 5, 0, 129], 17, 70, 300, 64), ([1] * 70, 3, 33, 200, 128), ([2, 500], 1, 300, 129, 128),
+    ([4] * 48, 5, 2500, 260, 64), ([3, 0, 5] * 16, 5, 2500, 264, 32)])
 def test_gemm_fp4_grouped(dtype, counts, pad, n, k, group):
     g = gen(sum(counts) + n)
     experts, rows = len(counts), sum(counts) + pad

@@ -197,10 +197,11 @@ __global__ __launch_bounds__(1024) void k_layer_norm_means(LayerNormBwdArgs a)
             for (int k = 0; k < VE; ++k)
                 g[k] *= w[k];
         }
+        const int n = inside<DT, TAIL>(v, hidden);
 #pragma unroll
         for (int k = 0; k < VE; ++k) {
             s[0] += g[k];
-            s[1] += g[k] * ((x[k] - mean) * rstd);
+            s[1] += g[k] * (k < n ? (x[k] - mean) * rstd : 0.0f);
         }
     }
     block_sums<2>(s, lds, turn);
@@ -334,9 +335,11 @@ __global__ __launch_bounds__(WG, 2) void k_layer_norm_backward(LayerNormBwdArgs 
             unpack<DT>(whole(now.dz[u]), g[u]);
             unpack<DT>(whole(now.dh[u]), o[u]);
             unpack<DT>(w[u], wf);
+            const int n = inside<DT, TAIL>(tid + u * W, hidden);
 #pragma unroll
             for (int k = 0; k < VE; ++k) {
-                x[u][k] = (x[u][k] - mean) * rstd;   // past the row: some number, met by d_z = 0
+                // past the row d_z is 0, but mean rstd may be infinite
+                x[u][k] = k < n ? (x[u][k] - mean) * rstd : 0.0f;
                 acc_w[u * VE + k] = __builtin_fmaf(g[u][k], x[u][k], acc_w[u * VE + k]);
                 acc_b[u * VE + k] += g[u][k];
                 g[u][k] *= wf[k];

@@ -352,7 +352,8 @@ template <int DT, int G, int V>
 __global__ __launch_bounds__(256) void k_route_backward(RouteBwdArgs a)
 {
     constexpr int TW = kWave / G, VE = Elem<DT>::kVE, kWaves = 4;
-    constexpr uint32_t kNone = 0x7FFFDEADu;   // no choice: a NaN that no gradient has
+    constexpr uint32_t kNone = 0x7FFFDEADu;   // no choice; a gradient that is NaN is kNaN
+    constexpr uint32_t kNaN = 0x7FC00000u;
     __shared__ __align__(16) uint32_t grads[kWaves][TW * G * V];
     const int lane = lane_id(), wave = threadIdx.x / kWave, pos = lane % G, sub = lane / G;
     const int experts = a.experts, topk = a.topk;
@@ -403,7 +404,7 @@ __global__ __launch_bounds__(256) void k_route_backward(RouteBwdArgs a)
                     dw = a.d_weights[t0 * topk + i];
                 }
                 if (i < n && id >= 0 && id < experts)
-                    grad[i / topk * (G * V) + id] = __builtin_bit_cast(uint32_t, dw);
+                    grad[i / topk * (G * V) + id] = dw != dw ? kNaN : __builtin_bit_cast(uint32_t, dw);
             }
             wave_sync();
         }

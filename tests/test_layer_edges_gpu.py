@@ -1,5 +1,5 @@
-"""The layer norm at the edges of what its calls accept,
-against its float64 form (layer_ref.py)."""
+"""The router and the layer norm at the edges of what their calls accept,
+against their float64 forms (layer_ref.py) or plain arithmetic."""
 import pytest
 import torch
 
@@ -7,7 +7,7 @@ import allreduce_reduction_rx_amd as rx
 import layer_ref as R
 from block_ref import cast_bound
 from test_block_ops_gpu import DTYPES, gen, randn, within
-from test_layer_ops_gpu import RNG
+from test_layer_ops_gpu import F32, RNG
 
 pytestmark = pytest.mark.gpu
 
@@ -41,3 +41,34 @@ def test_layer_norm_gradient_of_large_equal_elements(power, eps, hidden, drop, d
         within(t, want[name][0], cast_bound(*want[name], dtype))
     for name, t in (("d_bias", sums[0]), ("d_w", sums[1]), ("d_b", sums[2])):
         within(t, *want[name])
+
+
+# ---- router: gradients that are NaN ---------------------------------------------------
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("renormalize", [False, True])
+@pytest.mark.parametrize("experts,topk", [(5, 2), (64, 8), (160, 6), (1000, 3)])
+def test_route_gradient_of_every_nan(experts, topk, renormalize, dtype):
+    """A NaN of a choice's gradient makes its token's gradient NaN, whatever the NaN's bits: of every element, with
+    renormalize of the chosen ones. The other tokens' stay as they are."""
+    bits = [0x7FFFDEAD, 0x7FC00000, 0x7F800001, 0x7FFFFFFF, -1, 0xFF800001 - (1 << 32)]
+    g, tokens = gen(experts), 2 * len(bits) + 1
+    x = randn(g, tokens, experts).to(dtype).cuda()
+    ids, weights, lse = torch.empty(tokens, topk, dtype=torch.int32, device="cuda"), torch.empty(tokens, topk, **F32), torch.empty(tokens, **F32)
+    rx.rx_moe_route(x, ids, weights, renormalize=renormalize, lse=lse)
+    dw = randn(g, tokens, topk).cuda()
+    clean, d = torch.empty_like(x), torch.empty_like(x)
+    rx.rx_moe_route_backward(x, ids, lse, None, dw, None, clean, renormalize=renormalize)
+    assert bool(clean.isfinite().all())
+    at = torch.arange(1, 2 * len(bits), 2, device="cuda")
+    dw.view(torch.int32)[at, at % topk] = torch.tensor(bits, dtype=torch.int32, device="cuda")
+    assert int(dw.isnan().sum()) == len(bits)
+    rx.rx_moe_route_backward(x, ids, lse, None, dw, None, d, renormalize=renormalize)
+    bad = torch.zeros(tokens, experts, dtype=torch.bool, device="cuda")
+    if renormalize:
+        bad[at[:, None], ids[at].long()] = True
+    else:
+        bad[at] = True
+    assert torch.equal(d.isnan(), bad)
+    others = torch.arange(0, tokens, 2, device="cuda")
+    assert torch.equal(d[others], clean[others])

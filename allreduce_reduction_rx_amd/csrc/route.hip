@@ -84,19 +84,22 @@ __device__ __forceinline__ void put_losses(const RouteArgs& a, uint32_t n, float
     a.losses[1] = z * inv;
 }
 
-template <int V> constexpr int kRouteWaves = V == 16 ? 8 : 16;   // at most: what the registers allow
+// A workgroup's waves at most: with sums what the registers allow, without four.
+template <int V, bool SUMS> constexpr int kRouteWaves = !SUMS ? 4 : V == 16 ? 8 : 16;
 
 template <int DT, int G, int V, bool SUMS>
-__global__ __launch_bounds__(kRouteWaves<V> * kWave) void k_route(RouteArgs a)
+__global__ __launch_bounds__((kRouteWaves<V, SUMS> * kWave)) void k_route(RouteArgs a)
 {
     constexpr int TW = kWave / G;                                // tokens of a wave
     constexpr int MOST = V * G < kMaxTopk ? V * G : kMaxTopk;    // choices of a token
-    constexpr int W = kRouteWaves<V>;
+    constexpr int W = kRouteWaves<V, SUMS>;
     struct Pick {
         int id;
         uint32_t key;
     };
     __shared__ Pick picks[W][TW * MOST];
+    // without sums a CU has room for as many workgroups as the registers leave (eight, or four)
+    static_assert(SUMS || sizeof(picks) * (V == 16 ? 4 : 8) <= 160 * 1024, "");
     __shared__ uint32_t sums[SUMS ? 2 : 1][SUMS ? W : 1][SUMS ? V * G : 1];
     __shared__ uint32_t totals[W][2];
     __shared__ float dots[W];
@@ -482,7 +485,7 @@ Spread spread(size_t tokens, int experts, bool sums)
         return tokens ? (tokens + per - 1) / per : 1;
     };
     const int v = experts > 512 || units_of(8) > 12 * all ? 16 : 8;
-    const size_t units = units_of(v), most = !sums ? 4 : v == 16 ? 8 : 16;
+    const size_t units = units_of(v), most = !sums ? kRouteWaves<8, false> : v == 16 ? kRouteWaves<16, true> : kRouteWaves<8, true>;
     size_t w = units < most ? units : most;
     if (sums && units > most) {   // every CU before a second wave on one
         w = (units + cus - 1) / cus;

@@ -11,7 +11,8 @@ serve(): one step with 4-bit experts, without dropout.
 train(): the same block in BF16 with dropout, and the gradient of its outputs
 and of the router's two losses down to the logits, the tokens, the residual
 stream, the bias and the norm's weights.
-Both are compared with plain torch in float64.
+Both are compared with plain torch in float64, serve() with products of the weights
+that its codes stand for, so that what is off is the block's, not the quantization's.
 """
 import os
 import sys
@@ -76,6 +77,13 @@ def quantized(w):
     return codes[:, :, :(k + 1) // 2], scales
 
 
+def values(codes, scales, k):
+    """The weights that codes and scales stand for, in float64."""
+    level = torch.tensor([0, 0.5, 1, 1.5, 2, 3, 4, 6], dtype=torch.float64, device="cuda")
+    code = torch.stack([codes & 15, codes >> 4], -1).flatten(-2)[..., :k].long()
+    return torch.cat([level, -level])[code] * scales.double().repeat_interleave(GROUP, -1)[..., :k]
+
+
 def serve(b):
     """h and z of one step, from weights quantized beforehand."""
     up, down = [quantized(w) for w in b.up], [quantized(w) for w in b.down]
@@ -137,11 +145,10 @@ def kept(b):
     return out.double()
 
 
-def plain(b, d_h, d_z, mask):
-    """The block, its losses and its gradients in float64, every token through its experts."""
+def plain(b, d_h, d_z, mask, up, down):
+    """The block, its losses and its gradients in float64, every token through its experts, whose weights are up and down."""
     d = lambda t: t.double().requires_grad_()
     x, logits, res, bias, w, beta = (d(t) for t in (b.x, b.logits, b.residual, b.bias, b.w, b.b))
-    up, down = torch.cat(b.up).double(), torch.cat(b.down).double()
     live = b.mask.double()
     top, ids = torch.topk(logits, b.topk, dim=1)
     weights = torch.softmax(top, dim=1) * live[:, None]
@@ -168,10 +175,10 @@ def off(got, want):
 def main():
     b = Block()
     d_h, d_z = torch.randn_like(b.x), torch.randn_like(b.x)
-    h, z, _, _ = plain(b, d_h, d_z, 1.0)
+    h, z, _, _ = plain(b, d_h, d_z, 1.0, *(torch.cat([values(*quantized(w), w.shape[-1]) for w in ws]) for ws in (b.up, b.down)))
     sh, sz = serve(b)
     report = {"serve h": off(sh, h), "serve z": off(sz, z)}
-    h, z, losses, g = plain(b, d_h, d_z, kept(b))
+    h, z, losses, g = plain(b, d_h, d_z, kept(b), torch.cat(b.up).double(), torch.cat(b.down).double())
     th, tz, tl, tg = train(b, d_h, d_z)
     report.update({"train h": off(th, h), "train z": off(tz, z), "train losses": off(tl, losses)})
     report.update({f"train {k}": off(tg[k], g[k]) for k in g})

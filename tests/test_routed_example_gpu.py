@@ -29,3 +29,13 @@ def test_routed_example():
         # Two such products, after one another, h's and z's halves: sqrt(2) x 0.13 x
         # 5 = 0.92 at most for the block's result, less in h, where the residual joins.
         assert off < (0.05 + 0.92 if name.startswith("serve") else 0.05), (name, off)
+
+
+def test_routed_example_serves_the_weights_that_its_codes_stand_for():
+    """Compared with the products of the quantized weights, a serving step is off by its roundings alone: the limit of
+    the training step above (it has no more of them)."""
+    spec = importlib.util.spec_from_file_location("routed_block", os.path.join(ROOT, "examples", "routed_block.py"))
+    m = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(m)
+    report = m.main()
+    assert report["serve h"] < 0.05 and report["serve z"] < 0.05, report

@@ -15,9 +15,10 @@ __device__ __forceinline__ void fp4_scale(float a, float& s, float& r)
     r = !finite ? 0.0f : degenerate ? 1.0f : rv;
 }
 
-// A workgroup a row, a lane a vector: 4 to 32 neighbouring lanes have a group. Bytes
-// bound it: 8192 x 8192 takes 42 us in BF16 (4.0 TB/s), 57 in FP32 (5.3), once
-// for weights that are then multiplied many times.
+// A workgroup a row, a lane a vector: 4 to 32 neighbouring lanes have a group. 8192 x 8192
+// takes 59 us in FP32 (5.2 TB/s), which the bytes bound, and 43 in BF16 (4.0): there a thread's
+// four loads, each waited for by its group's maximum before the next goes out (waves
+// wait 72% of their cycles). Once for weights that are then multiplied many times.
 template <int DT, bool TAIL>
 __global__ __launch_bounds__(256) void k_quant_fp4(QuantFp4Args a)
 {

@@ -344,12 +344,15 @@ __device__ __forceinline__ void open_stage(bool next)
 
 // Few rows: 16 TT rows x 16 NS channels a workgroup of KS x NS waves, KC of k a
 // stage, DX - 1 stages of rows and DW - 1 of weights on their way. How many pays is
-// measured: 64 x 8192 x 8192 with weights from memory 34.5 us with one of each and 27.5
+// measured: 64 x 8192 x 8192 in groups of 32 with weights from memory 34.5 us with one of each and 27.5
 // with two of weights, 13 x 4096 x 8192 12.0 with one of each, 9.1 with two and three, but
 // 256 rows of 64 experts, whose three or four workgroups a CU wait for each other less, 17.8
 // with one and 21 with two. A wave has 16 channels and every KS-th part of a
-// stage; the KS sums meet in LDS in their order. Bound by the weights' bytes, and by
-// the rows that every workgroup reads again (1 x 8192 x 8192: 9.2 us for 36 MB; 32 rows: 16).
+// stage; the KS sums meet in LDS in their order. 1 x 8192 x 8192 takes 10.3 us with the weights'
+// 36 MB from memory and 9.4 with them in the last-level cache, 32 rows 16.1 and 14.7 (their rows,
+// which every workgroup reads again by way of L2, are less than half of that): bound by the start and
+// the end, and by stages whose wait, LDS reads, conversions and products follow each
+// other with two waves a SIMD (waves wait 61% and 47% of their cycles, matrix cores are busy 7% and 9%).
 template <int DT, int GR, int TT, int TR, int KS, int NS, int KC, int DX, int DW, bool WHOLE>
 __global__ __launch_bounds__(KS * NS * kWave) void k_gemm_fp4_stream(GemmFp4Args a)
 {
@@ -471,8 +474,8 @@ __global__ __launch_bounds__(KS * NS * kWave) void k_gemm_fp4_stream(GemmFp4Args
 // take every eighth chunk of 128 of k; the sums meet in LDS in their order. All
 // from memory to registers, D chunks ahead, the rows before the weights: loads
 // return in order, so a row's chunk that was asked for after the weights would
-// wait for them. Half the start of k_gemm_fp4_stream (13 x 1000 x 2051: 6.7
-// against 7.9 us), but 16 lines of the cache a load (16 x 8192 x 8192: 39 against 21).
+// wait for them. Half the start of k_gemm_fp4_stream (13 x 1000 x 2051: 7.2
+// against 8.3 us), but 16 lines of the cache a load (16 x 8192 x 8192: 40 against 21).
 template <int DT, int GR>
 __global__ __launch_bounds__(8 * kWave) void k_gemm_fp4_few(GemmFp4Args a)
 {
@@ -551,8 +554,9 @@ __device__ __forceinline__ void keep(f32x4 (&x)[N])
 // the scales join the sums of the step before, and a later stage asks for its share:
 // all loads at once would hold the wave up for as long as the cache takes them. A stage
 // is opened before the one before has ended, so that its first steps find their
-// operands. 1024 x 8192 x 8192: 118 to 129 us (1.07 to 1.17 PFLOP/s), 140 with stages one after
-// the other, 160 in 128 x 128 tiles whose waves loaded their weights themselves.
+// operands. 1024 x 8192 x 8192 with operands in the last-level cache: 118 to 122 us (1.13 to 1.17 PFLOP/s),
+// 140 with stages one after the other, 160 in 128 x 128 tiles whose waves loaded their weights
+// themselves; with operands from memory 128 to 133 (groups of 32: 171).
 template <int GR>
 __global__ __launch_bounds__(8 * kWave, 2) void k_gemm_fp4_tile(GemmFp4Args a)
 {
@@ -792,8 +796,10 @@ struct Kind {
 };
 
 // Estimated time. The kinds' figures are measured at 8192 and 4096 of k, with
-// groups of 128 (32: 5 to 30% more, alike for all). CUs that are full, round by round, and
-// a last round that fills up from `alone` to `full`.
+// groups of 128 (32: 5 to 35% more, alike for all) and weights in the last-level cache. CUs that
+// are full, round by round, and a last round that fills up from `alone` to `full`.
+// Up to four rows two workgroups of 16 x 32 do share a CU, which `per_cu` leaves out: beyond
+// two rounds of them it estimates too much.
 inline double estimate(const GemmFp4Args& a, const Kind& x, double rows)
 {
     const double cus = device_cu_count();
@@ -820,28 +826,41 @@ inline double estimate(const GemmFp4Args& a, const Kind& x)
     return a.offsets ? 0.5 * (all + estimate(a, x, 0.5 * (double)a.rows)) : all;
 }
 
-// The kinds, and where another would go wrong (us, groups of 128):
-//   BF16                          16x16 16x32 16x64 32x32 32x128 64x32 64x128 128x256
-//   13 x 4096 x 8192                8.6  10.4
-//   16 x 8192 x 8192               15.5  11.8  38.9
-//   32 x 8192 x 8192                                 15.5  30.7
-//   64 x 8192 x 8192                                              24.5   49
-//   64 x 4096 x 4096                            9.5               12.5
-//   128 x 8192 x 8192                                     34.9    42     50     99
-//   512 x 8192 x 8192                                              159   96     111
-//   1024 x 8192 x 8192                                                  179     124
-//   64 experts x 4 x 4096 x 4096          190   120
-//   64 experts x 24 x 4096 x 4096                     270   162          231    269
-//   64 experts x 48 x 4096 x 4096                           254   415    252    276
-//   64 experts x 256 x 4096 x 4096                                       805    580
-//   FP32                            few  16x32 16x64        32x128       64x128 parts
-//   13 x 1000 x 2051                6.7   7.9
-//   16 x 8192 x 8192                 39    21
-//   128 x 8192 x 8192                                         72          133
-//   512 x 8192 x 8192                                        228          190
-//   64 experts x 4 x 4096 x 4096          296   180
-//   12 experts x 129 x 2100 x 2056                            67           85
-//   64 experts x 48 x 4096 x 4096                            481          397
+// The kinds, and where another would go wrong (us, groups of 128; dense ones with weights in the
+// last-level cache and, behind the stroke, from memory, where those of 64 experts are always):
+//   BF16                          16x16     16x32     16x64     32x32     32x128    64x32     64x128    128x256
+//   1 x 1024 x 8192               6.6/6.7   8.8/8.8
+//   1 x 6144 x 8192               8.8/9.7   8.8/9.9   23/30
+//   1 x 8192 x 8192               9.1/10.4  9.4/10.4  24/29
+//   1 x 14336 x 4096              9.4/11.0  7.4/9.4   13/17
+//   1 x 14336 x 8192              16/18     14/16     24/31
+//   1 x 28672 x 4096              16/18     15/16     15/18               18/24               27/28
+//   1 x 28672 x 8192              26/30     24/28     28/35               33/47               51/53
+//   13 x 4096 x 8192              8.6/9.5   10.2/11.4
+//   16 x 8192 x 8192              15/17     11.2/12.6 23/29
+//   32 x 1024 x 8192              8.2/8.3   10/10               14/14
+//   32 x 6144 x 8192              22/24     19/21     24/30     14/15     32/46
+//   32 x 8192 x 8192              28/31     19/21     24/29     14/16     32/43
+//   32 x 14336 x 8192             48/52     36/39     27/32     27/28     32/46     39/41
+//   32 x 28672 x 8192             94/101    63/68     42/58     52/54     34/49     77/79     51/57
+//   64 x 8192 x 8192                                                                22/24     50/56
+//   64 x 4096 x 4096                                            8.6/9.4             11.6/12.4
+//   128 x 8192 x 8192                                                     32/41     41/42     50/55     102/111
+//   512 x 8192 x 8192                                                               158/162   88/96     104/111
+//   1024 x 8192 x 8192                                                                        171/179   120/128
+// (28672 channels of one row get 32 x 128, the one choice here that is wrong by more than a tenth.)
+//   64 experts x 4 x 4096 x 4096            190       120
+//   64 experts x 24 x 4096 x 4096                               270       162                 231       269
+//   64 experts x 48 x 4096 x 4096                                         254       415       252       276
+//   64 experts x 256 x 4096 x 4096                                                            805       580
+//   FP32                            few       16x32     16x64     32x128    64x128 parts
+//   13 x 1000 x 2051                7.2/7.4   8.3/8.2
+//   16 x 8192 x 8192                40/41     21/23
+//   128 x 8192 x 8192                                             71/73     137/139
+//   512 x 8192 x 8192                                             234/236   188/194
+//   64 experts x 4 x 4096 x 4096            296       180
+//   12 experts x 129 x 2100 x 2056                              67        85
+//   64 experts x 48 x 4096 x 4096                               481       397
 template <int DT, int GR>
 hipError_t launch_fp4(const GemmFp4Args& in, hipStream_t s)
 {
@@ -853,7 +872,7 @@ hipError_t launch_fp4(const GemmFp4Args& in, hipStream_t s)
                               {16, 16, 1, 2.0, 2.0}};
     const bool whole = DT == 1 && (uintptr_t)a.a % 16 == 0 && a.ld_a % 8 == 0 && a.k % 8 == 0;
     const Kind* kinds = DT == 0 ? kFp32 : kBf16;
-    const int n = DT == 0 ? 5 : whole ? 8 : 6;   // rows by way of registers gain nothing from larger tiles
+    const int n = DT == 0 ? 5 : whole ? 8 : 6;   // rows by way of registers have no larger tile: 1024 x 8192 x 8191 takes 190 us
     int best = 0;
     double cost = 1e301;
     for (int i = 0; i < n; ++i) {
@@ -872,7 +891,7 @@ hipError_t launch_fp4(const GemmFp4Args& in, hipStream_t s)
         default: return launch_grid(a, (const void*)k_gemm_fp4_few<0, GR>, "k_gemm_fp4_few", 16, 16, 8 * kWave, s);
         }
     } else if (whole) {
-        const bool four = a.rows <= 4;   // fewer rows to load: 1 x 8192 x 8192 9.9 against 11.2 us
+        const bool four = a.rows <= 4;   // fewer rows to load: 4 x 8192 x 8192 9.4 us, 10.3 from memory; 5 rows 10.6 and 11.4
         switch (best) {
         case 0: return four ? launch_stream<1, GR, 1, 4, 4, 2, 1024, 3, 3, true>(a, "k_gemm_fp4_stream 16x32, four rows", s) : launch_stream<1, GR, 1, 16, 4, 2, 1024, 3, 3, true>(a, "k_gemm_fp4_stream 16x32", s);
         case 1: return launch_stream<1, GR, 1, 16, 1, 4, 256, 2, 2, true>(a, "k_gemm_fp4_stream 16x64", s);

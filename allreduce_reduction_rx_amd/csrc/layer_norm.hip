@@ -5,7 +5,7 @@
 // every output written once. The variance is that of the differences from the
 // mean: a second sum over the row, but right for rows whose mean is large
 // against their spread. HBM-bound: 16384 x 8192 BF16 with two sources, residual,
-// bias and dropout takes 217 us for 1.34 GB read and written (6.2 TB/s); the
+// bias and dropout takes 220 us for 1.34 GB read and written (6.1 TB/s); the
 // generator's 40 multiplications a vector run while the memory does.
 #include "norm_common.hpp"
 #include "philox.hpp"
@@ -284,8 +284,8 @@ __global__ __launch_bounds__(256) void k_layer_norm_columns(LayerNormBwdArgs a)
 // each where TEAMS; the next row's loads go out as soon as this row's are
 // unpacked, before its sums and stores, and the next two rows' where a workgroup has a CU
 // for itself (16384 x 8192 BF16 with dropout, forward and gradient 474 us, 486 with one; 8192 x 4096,
-// two workgroups a CU, 89 and 87). 16384 x 8192 BF16 with dropout and all outputs: 245 us for
-// 1.34 GB (5.5 TB/s), 340 by k_layer_norm_means and k_layer_norm_columns, which read h and
+// two workgroups a CU, 89 and 87). 16384 x 8192 BF16 with dropout and all outputs: 250 us for
+// 1.34 GB (5.4 TB/s), 340 by k_layer_norm_means and k_layer_norm_columns, which read h and
 // d_z twice.
 template <int DT, bool TAIL, int NV, int WG, bool TEAMS, bool DROP>
 __global__ __launch_bounds__(WG, 2) void k_layer_norm_backward(LayerNormBwdArgs a)
